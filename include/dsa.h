@@ -392,6 +392,177 @@ dsa_status dsa_decode_noalloc(const dsa_params* params, const dsa_ragged* ragged
                               void* stream);
 
 /*
+ * Around the layer: what fills its inputs and its second branch.  In a hybrid model whose
+ * layers mix sparse attention with linear attention ([HSA] "Indexer + Top-K: How Fine-Grained
+ * Sparse Attention Works", last line of the pseudocode; [FGS] "How Indexer + Top-K Works at
+ * Runtime", step 3), dsa_rope_append turns the projections of the new tokens into q, q_idx and
+ * the rows of the caches, and dsa_short_conv + dsa_gated_delta_prefill / _decode compute the
+ * linear branch, `other` of dsa_sparse_attn_gated_mix.  The pages name both and define neither;
+ * the formulas below are the ones this library implements.
+ * The conventions at the top hold; rows of a padded batch (q_offsets[batch] .. total_q-1) are
+ * neither read nor written.
+ */
+
+/* Pairs of a rotated part of r dimensions: (i, i + r/2), or (2i, 2i + 1). */
+typedef enum { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1 } dsa_rope_layout;
+
+/* Angle per position of pair i, from f_i = theta^(-2i/r):
+ *   NONE      f_i
+ *   LINEAR    f_i / factor
+ *   NTK       theta' = theta * factor^(r / (r - 2)) in place of theta (r > 2)
+ *   BY_PARTS  with n_i = orig_len * f_i / (2 pi) turns over the length trained on and
+ *             y = clamp((n_i - beta_slow) / (beta_fast - beta_slow), 0, 1):
+ *             f_i * (y + (1 - y) / factor) */
+typedef enum {
+  DSA_ROPE_SCALE_NONE = 0,
+  DSA_ROPE_SCALE_LINEAR = 1,
+  DSA_ROPE_SCALE_NTK = 2,
+  DSA_ROPE_SCALE_BY_PARTS = 3
+} dsa_rope_scaling;
+
+typedef struct {
+  int32_t layout;          /* dsa_rope_layout                                            */
+  int32_t scaling;         /* dsa_rope_scaling                                           */
+  int32_t rot_dim;         /* rotated dimensions of a q or k head, 0 .. head_dim         */
+  int32_t rot_offset;      /* the first of them                                          */
+  int32_t idx_rot_dim;     /* the same for the heads of q_idx and k_idx, 0 .. idx_dim    */
+  int32_t idx_rot_offset;
+  double theta;            /* > 0                                                        */
+  double factor;           /* > 0 (not read for NONE)                                    */
+  double orig_len;         /* BY_PARTS: > 0                                              */
+  double beta_fast;        /* BY_PARTS: beta_fast > beta_slow                            */
+  double beta_slow;
+  double magnitude;        /* factor on every rotated pair; 0 selects 1                  */
+  int64_t q_row_stride;    /* elements from one packed row of an input to the next;      */
+  int64_t k_row_stride;    /* 0: packed.  For slices of a fused projection's output.     */
+  int64_t v_row_stride;
+  int64_t q_idx_row_stride;
+  int64_t k_idx_row_stride;
+} dsa_rope_params;
+
+/* Inputs (bf16, one row per packed query row) and where they go.  An input that is NULL is
+ * left out with its output. */
+typedef struct {
+  const void* q;      /* [total_q, Hq, d]                                                */
+  const void* k;      /* [total_q, Hkv, d]                                               */
+  const void* v;      /* [total_q, Hkv, d]                                               */
+  const void* q_idx;  /* [total_q, H_i, D_i]                                             */
+  const void* k_idx;  /* [total_q, H_i, D_i]                                             */
+  void* q_out;        /* bf16 [total_q, Hq, d]; q itself (packed) for in place           */
+  void* k_cache;      /* bf16 [total_kv, Hkv, d]                                         */
+  void* v_cache;      /* bf16 [total_kv, Hkv, d]                                         */
+  void* q_idx_out;    /* params->idx_dtype [total_q, H_i, D_i]; q_idx itself if bf16     */
+  void* k_idx_cache;  /* params->idx_dtype [total_kv, H_i, D_i]                          */
+} dsa_rope_buffers;
+
+/*
+ * Rotary positions of a batch's new rows and their append to the caches, in one pass.  Query i
+ * of sequence b is at p = L_b - Q_b + i (kv_offsets count the new rows), so the call precedes
+ * dsa_prefill / dsa_decode with the same dsa_ragged.  A pair (x, y) turns by a = pos * f_i:
+ *   x' = magnitude * (x cos a - y sin a),  y' = magnitude * (x sin a + y cos a)
+ * and dimensions outside the rotated part are copied.  q and q_idx go to q_out and q_idx_out;
+ * k, k_idx (turned) and v (copied) to the cache row of position p.  With idx_dtype
+ * DSA_FP8_E4M3 an indexer element x is stored as e4m3(x / idx_scale_q) or e4m3(x /
+ * idx_scale_k), to nearest even, saturating at +-448.
+ *   positions int32 [total_q] or NULL: the angle's position of each row, any sign (NULL: p).
+ *             The cache row is that of p either way.
+ *   err_count int32 [1] or NULL: incremented once per row whose cache row is outside the
+ *             arrays (a page id outside the block table's range, a sequence with more queries
+ *             than cache positions); nothing is appended for such a row.
+ * Angles are formed and reduced in 64 bits; the rotation is fp32, rounded once.
+ * Supported: head_dim 128, idx_dim 64, 1 .. 4 indexer heads, any Hq and Hkv; rotated
+ * dimensions a multiple of 16, their offset a multiple of 8.  Of dsa_params only the head
+ * counts and dimensions, idx_dtype and idx_scale_* are read (those of absent inputs are not).
+ * Requirements: every buffer 16-byte aligned, row strides multiples of 8; an output overlaps
+ * nothing else in the call but, exactly, its own packed input; positions of one sequence's
+ * rows do not share cache rows with another's new rows.
+ */
+dsa_status dsa_rope_append(const dsa_params* params, const dsa_ragged* ragged,
+                           const dsa_rope_params* rope, const dsa_rope_buffers* buffers,
+                           const int32_t* positions, int32_t* err_count, void* stream);
+
+typedef struct {
+  int32_t channels;      /* a multiple of 8                                              */
+  int32_t width;         /* W: 2 .. 4                                                    */
+  int32_t silu;          /* act(y) = y / (1 + e^-y); 0: act(y) = y                       */
+  int32_t n_states;      /* slots of state_in / state_out                                */
+  int64_t x_row_stride;  /* elements; 0: packed                                          */
+  int64_t out_row_stride;
+} dsa_conv_params;
+
+/*
+ * Short causal convolution, each channel over its own last W rows, for a ragged batch (prefill
+ * chunks, single tokens, both):
+ *   out[t,c] = act(bias[c] + sum_{j=0}^{W-1} weight[c,j] * x[t-W+1+j, c])
+ * A sequence's rows before its first come from its state: the W - 1 rows before, newest last.
+ *   x, out      bf16 [total_q, channels]
+ *   weight      bf16 [channels, W]; bias bf16 [channels] or NULL
+ *   state_in    bf16 [n_states, W-1, channels] or NULL (zeros)
+ *   state_out   the same or NULL (not kept): receives the last W - 1 rows of (state, x), also
+ *               of a sequence without rows.  May be state_in.
+ *   state_index int32 [batch] or NULL (sequence b uses slot b): the slot of each sequence.
+ *               Slots of one call are distinct; a sequence whose slot is outside 0 ..
+ *               n_states-1 starts from zeros and its state is not kept.
+ * Sums are fp32, the output is rounded once.  Only batch, q_offsets and total_q of dsa_ragged
+ * are read.  Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps
+ * neither x nor a state; state_out is state_in or does not overlap it.
+ */
+dsa_status dsa_short_conv(const dsa_conv_params* params, const dsa_ragged* ragged, const void* x,
+                          const void* weight, const void* bias, const void* state_in,
+                          void* state_out, const int32_t* state_index, void* out, void* stream);
+
+typedef struct {
+  int32_t n_k_heads;     /* Hk                                                           */
+  int32_t n_v_heads;     /* Hv: a multiple of Hk; value head h reads key head h/(Hv/Hk)  */
+  int32_t head_dim;      /* d of q, k and v: 128                                         */
+  int32_t qk_norm;       /* not 0: q and k are divided by sqrt(sum x^2 + norm_eps)       */
+  float norm_eps;        /* > 0 with qk_norm                                             */
+  float scale;           /* 0 selects 1/sqrt(d)                                          */
+  int32_t n_states;      /* slots of state_in / state_out                                */
+  int32_t reserved;      /* 0                                                            */
+  int64_t q_row_stride;  /* elements; 0: packed                                          */
+  int64_t k_row_stride;
+  int64_t v_row_stride;
+} dsa_delta_params;
+
+/*
+ * The gated delta rule for a ragged batch.  Per value head, with the state S [dv, dk]:
+ *   S_t = e^g_t S_{t-1} + beta_t (v_t - e^g_t S_{t-1} k_t) k_t^T,  out_t = scale * S_t q_t
+ *   q, k        bf16 [total_q, Hk, d]; v bf16 [total_q, Hv, d]
+ *   g, beta     fp32 [total_q, Hv]; g is the logarithm of the decay (<= 0; -inf forgets all)
+ *   out         bf16 [total_q, Hv, d]: with Hv = Hq and d = head_dim, `other` of
+ *               dsa_sparse_attn_gated_mix
+ *   state_in    fp32 [n_states, Hv, dv, dk] or NULL (zeros)
+ *   state_out   the same or NULL (not kept): the state after the sequence's last token (that
+ *               before it, for a sequence without tokens).  May be state_in.
+ *   state_index int32 [batch] or NULL, as for dsa_short_conv.
+ * dsa_gated_delta_prefill takes any Q_b: sequences of up to 16 tokens run token by token, longer
+ * ones in chunks of 64 (the state stays fp32; operands of the tensor-core products enter in
+ * bf16 pieces that keep the state within about 1e-6 of itself).  A sequence's results depend
+ * neither on the rest of the batch nor on the workspace's size.
+ * dsa_gated_delta_decode is for at most one token per sequence (max_q_len <= 1) and takes no
+ * workspace.
+ *   workspace   device, 256-byte aligned, ws_bytes >= the minimum of
+ *               dsa_gated_delta_workspace_size (one head's chunks; the heads run in as many
+ *               passes as that needs, the recommended size holds all).  0 bytes, and NULL, when
+ *               max_q_len <= 16.
+ * Only batch, q_offsets, max_q_len, total_q and q_offsets_host of dsa_ragged are read.
+ * Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps no input and
+ * no state; state_out is state_in or does not overlap it.
+ */
+dsa_status dsa_gated_delta_workspace_size(const dsa_delta_params* params, const dsa_ragged* ragged,
+                                          size_t* min_bytes, size_t* rec_bytes);
+dsa_status dsa_gated_delta_prefill(const dsa_delta_params* params, const dsa_ragged* ragged,
+                                   const void* q, const void* k, const void* v, const float* g,
+                                   const float* beta, const float* state_in, float* state_out,
+                                   const int32_t* state_index, void* out, void* workspace,
+                                   size_t ws_bytes, void* stream);
+dsa_status dsa_gated_delta_decode(const dsa_delta_params* params, const dsa_ragged* ragged,
+                                  const void* q, const void* k, const void* v, const float* g,
+                                  const float* beta, const float* state_in, float* state_out,
+                                  const int32_t* state_index, void* out, void* stream);
+
+/*
  * Device status word of the current device: synchronises `stream`, stores the status
  * recorded by kernels since the last clear (DSA_OK or DSA_ERR_TIMEOUT) in *status (host),
  * and clears it when clear != 0.

@@ -19,6 +19,8 @@ from . import _build
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA, \
     DSA_ERR_TIMEOUT = range(6)
 DSA_BF16, DSA_FP8_E4M3 = 0, 1
+DSA_ROPE_HALF, DSA_ROPE_INTERLEAVED = 0, 1
+DSA_ROPE_SCALE_NONE, DSA_ROPE_SCALE_LINEAR, DSA_ROPE_SCALE_NTK, DSA_ROPE_SCALE_BY_PARTS = range(4)
 
 LIB_PATH = _build.LIB
 
@@ -65,13 +67,53 @@ def layer_buffers(t: dict) -> LayerBuffers:
     return LayerBuffers(*[_ptr(t.get(k)) for k in LAYER_BUFFER_KEYS])
 
 
+class RopeParams(ctypes.Structure):
+    _fields_ = [
+        ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("rot_offset", ctypes.c_int32),
+        ("idx_rot_dim", ctypes.c_int32), ("idx_rot_offset", ctypes.c_int32),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+        ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+        ("magnitude", ctypes.c_double),
+        ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64), ("q_idx_row_stride", ctypes.c_int64),
+        ("k_idx_row_stride", ctypes.c_int64),
+    ]
+
+
+class RopeBuffers(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "q", "k", "v", "q_idx", "k_idx", "q_out", "k_cache", "v_cache", "q_idx_out",
+        "k_idx_cache")]
+
+
+class ConvParams(ctypes.Structure):
+    _fields_ = [
+        ("channels", ctypes.c_int32), ("width", ctypes.c_int32), ("silu", ctypes.c_int32),
+        ("n_states", ctypes.c_int32), ("x_row_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64),
+    ]
+
+
+class DeltaParams(ctypes.Structure):
+    _fields_ = [
+        ("n_k_heads", ctypes.c_int32), ("n_v_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("qk_norm", ctypes.c_int32),
+        ("norm_eps", ctypes.c_float), ("scale", ctypes.c_float),
+        ("n_states", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64),
+    ]
+
+
 EXPORTS = [
     "dsa_status_string", "dsa_version", "dsa_index_scores", "dsa_topk",
     "dsa_sparse_attn_gated", "dsa_workspace_size", "dsa_prefill", "dsa_decode",
     "dsa_device_status", "dsa_launch_count", "dsa_stage_timing", "dsa_stage_times",
     "dsa_decode_noalloc", "dsa_index_topk", "dsa_index_topk_workspace_size",
     "dsa_sparse_attn_gated_mix", "dsa_index_topk_blocks", "dsa_index_topk_blocks_workspace_size",
-    "dsa_prefill_from_host", "dsa_fused_rows",
+    "dsa_prefill_from_host", "dsa_fused_rows", "dsa_rope_append", "dsa_short_conv",
+    "dsa_gated_delta_workspace_size", "dsa_gated_delta_prefill", "dsa_gated_delta_decode",
 ]
 
 
@@ -107,6 +149,13 @@ def _load():
     L.dsa_fused_rows.restype = i64
     L.dsa_stage_timing.argtypes = [ctypes.c_int]
     L.dsa_stage_times.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64), ctypes.c_int]
+    L.dsa_rope_append.argtypes = [PP, RP, ctypes.POINTER(RopeParams), ctypes.POINTER(RopeBuffers),
+                                  vp, vp, vp]
+    L.dsa_short_conv.argtypes = [ctypes.POINTER(ConvParams), RP, vp, vp, vp, vp, vp, vp, vp, vp]
+    DP = ctypes.POINTER(DeltaParams)
+    L.dsa_gated_delta_workspace_size.argtypes = [DP, RP, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    L.dsa_gated_delta_prefill.argtypes = [DP, RP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.dsa_gated_delta_decode.argtypes = [DP, RP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     for name in ("dsa_index_scores", "dsa_topk", "dsa_sparse_attn_gated", "dsa_workspace_size",
                  "dsa_prefill", "dsa_decode", "dsa_decode_noalloc", "dsa_device_status",
                  "dsa_stage_timing",
@@ -311,6 +360,207 @@ def dsa_decode_noalloc(shape: LayerShape, rg: Ragged, q_idx, k_idx, w, q, k_cach
                                   _ptr(w), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(gate),
                                   _ptr(out), _ptr(idx_out), _ptr(err_count), _stream(stream)),
            "dsa_decode_noalloc")
+
+
+# ---------------------------------------------------------------- around the layer
+#
+# These take torch tensors whose rows may be slices of wider ones (a fused projection's output):
+# row strides come from the tensors, and types, sizes and the device are checked here, since the
+# library sees addresses only.
+
+@dataclass
+class RopeShape:
+    """Rotary layout, the rotated part of a head, and its frequencies (dsa_rope_params)."""
+    layout: int = DSA_ROPE_HALF
+    rot_dim: int = 128
+    idx_rot_dim: int = 64
+    rot_offset: int = 0
+    idx_rot_offset: int = 0
+    scaling: int = DSA_ROPE_SCALE_NONE
+    theta: float = 10000.0
+    factor: float = 1.0
+    orig_len: float = 4096.0
+    beta_fast: float = 32.0
+    beta_slow: float = 1.0
+    magnitude: float = 1.0
+
+
+@dataclass
+class ConvShape:
+    """Channels, taps and activation of the short convolution (dsa_conv_params)."""
+    channels: int
+    width: int = 4
+    silu: bool = True
+
+
+@dataclass
+class DeltaShape:
+    """Heads and numerics of the gated delta rule (dsa_delta_params)."""
+    n_k_heads: int
+    n_v_heads: int
+    head_dim: int = 128
+    qk_norm: bool = True
+    norm_eps: float = 1e-6
+    scale: float = 0.0
+
+
+def _bad(where: str, what: str):
+    raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {what}")
+
+
+def _tensor(where, name, t, dtype, shape, device) -> int:
+    """Address of a dense tensor of at least shape[0] rows and exactly the other sizes."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _bad(where, f"{name} is {t.dtype} on {t.device}, not {dtype} on cuda:{device}")
+    if t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != shape[1:]:
+        _bad(where, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        _bad(where, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _rows(where, name, t, dtype, shape, device):
+    """Address and row stride of a tensor whose rows are dense."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _bad(where, f"{name} is {t.dtype} on {t.device}, not {dtype} on cuda:{device}")
+    if t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != shape[1:]:
+        _bad(where, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    dense = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size > 1 and step != dense:
+            _bad(where, f"{name} has rows that are not dense (strides {t.stride()})")
+        dense *= size
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _device(stream) -> int:
+    import torch
+    device = torch.cuda.current_device()
+    if stream is not None and stream.device.index != device:
+        raise DsaError(DSA_ERR_INVALID_ARG, f"stream of {stream.device} while cuda:{device} is current")
+    return device
+
+
+def _index(where, name, t, n, device):
+    import torch
+    return None if t is None else _tensor(where, name, t, torch.int32, (n,), device)
+
+
+def dsa_rope_append(shape: LayerShape, rg: Ragged, rope: RopeShape, q=None, k=None, v=None,
+                    q_idx=None, k_idx=None, q_out=None, k_cache=None, v_cache=None,
+                    q_idx_out=None, k_idx_cache=None, positions=None, err_count=None, stream=None):
+    """Rotary positions of the batch's new rows: q and q_idx to q_out and q_idx_out, k, v and
+    k_idx to the cache rows of their positions.  Inputs left out leave their outputs out."""
+    import torch
+    where, device = "dsa_rope_append", _device(stream)
+    bf16 = torch.bfloat16
+    idx_type = torch.float8_e4m3fn if shape.idx_dtype == DSA_FP8_E4M3 else bf16
+    d, di = shape.head_dim, shape.idx_dim
+    nq, nkv, ni = shape.n_q_heads, shape.n_kv_heads, shape.n_idx_heads
+    src, strides, dst = [], [], []
+    for name, t, to_name, to, heads, dim, rows, kind in (
+            ("q", q, "q_out", q_out, nq, d, rg.total_q, bf16),
+            ("k", k, "k_cache", k_cache, nkv, d, rg.total_kv, bf16),
+            ("v", v, "v_cache", v_cache, nkv, d, rg.total_kv, bf16),
+            ("q_idx", q_idx, "q_idx_out", q_idx_out, ni, di, rg.total_q, idx_type),
+            ("k_idx", k_idx, "k_idx_cache", k_idx_cache, ni, di, rg.total_kv, idx_type)):
+        if t is None:
+            src.append(None), strides.append(0), dst.append(None)
+            continue
+        if to is None:
+            _bad(where, f"{name} without {to_name}")
+        p, step = _rows(where, name, t, bf16, (rg.total_q, heads, dim), device)
+        src.append(p), strides.append(step)
+        dst.append(_tensor(where, to_name, to, kind, (rows, heads, dim), device))
+    o = RopeParams(rope.layout, rope.scaling, rope.rot_dim, rope.rot_offset, rope.idx_rot_dim,
+                   rope.idx_rot_offset, rope.theta, rope.factor, rope.orig_len, rope.beta_fast,
+                   rope.beta_slow, rope.magnitude, *strides)
+    b = RopeBuffers(*src, dst[0], dst[1], dst[2], dst[3], dst[4])
+    p = shape.params()
+    _check(lib.dsa_rope_append(ctypes.byref(p), ctypes.byref(rg), ctypes.byref(o), ctypes.byref(b),
+                               _index(where, "positions", positions, rg.total_q, device),
+                               _index(where, "err_count", err_count, 1, device),
+                               _stream(stream)), where)
+
+
+def dsa_short_conv(conv: ConvShape, rg: Ragged, x, weight, out, bias=None, state_in=None,
+                   state_out=None, state_index=None, stream=None):
+    """Short causal convolution of x [total_q, channels] into out, rows before a sequence's
+    first from state_in [slots, width - 1, channels], the last ones to state_out."""
+    import torch
+    where, device = "dsa_short_conv", _device(stream)
+    bf16, c = torch.bfloat16, conv.channels
+    px, sx = _rows(where, "x", x, bf16, (rg.total_q, c), device)
+    po, so = _rows(where, "out", out, bf16, (rg.total_q, c), device)
+    pw = _tensor(where, "weight", weight, bf16, (c, conv.width), device)
+    pb = None if bias is None else _tensor(where, "bias", bias, bf16, (c,), device)
+    slots = [t.shape[0] for t in (state_in, state_out) if t is not None]
+    n = min(slots) if slots else 0
+    s0, s1 = (None if t is None else
+              _tensor(where, name, t, bf16, (n, conv.width - 1, c), device)
+              for name, t in (("state_in", state_in), ("state_out", state_out)))
+    p = ConvParams(c, conv.width, int(conv.silu), n, sx, so)
+    _check(lib.dsa_short_conv(ctypes.byref(p), ctypes.byref(rg), px, pw, pb, s0, s1,
+                              _index(where, "state_index", state_index, rg.batch, device), po,
+                              _stream(stream)), where)
+
+
+def _delta_params(delta: DeltaShape, n_states: int = 0, strides=(0, 0, 0)) -> DeltaParams:
+    return DeltaParams(delta.n_k_heads, delta.n_v_heads, delta.head_dim, int(delta.qk_norm),
+                       delta.norm_eps, delta.scale, n_states, 0, *strides)
+
+
+def _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out, state_index, device):
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    n, hk, hv, d = rg.total_q, delta.n_k_heads, delta.n_v_heads, delta.head_dim
+    pq, sq = _rows(where, "q", q, bf16, (n, hk, d), device)
+    pk, sk = _rows(where, "k", k, bf16, (n, hk, d), device)
+    pv, sv = _rows(where, "v", v, bf16, (n, hv, d), device)
+    pg = _tensor(where, "g", g, f32, (n, hv), device)
+    pb = _tensor(where, "beta", beta, f32, (n, hv), device)
+    po = _tensor(where, "out", out, bf16, (n, hv, d), device)
+    slots = [t.shape[0] for t in (state_in, state_out) if t is not None]
+    ns = min(slots) if slots else 0
+    s0, s1 = (None if t is None else _tensor(where, name, t, f32, (ns, hv, d, d), device)
+              for name, t in (("state_in", state_in), ("state_out", state_out)))
+    pi = _index(where, "state_index", state_index, rg.batch, device)
+    return _delta_params(delta, ns, (sq, sk, sv)), (pq, pk, pv, pg, pb, s0, s1, pi, po)
+
+
+def dsa_gated_delta_workspace_size(delta: DeltaShape, rg: Ragged):
+    p = _delta_params(delta)
+    mn, rec = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib.dsa_gated_delta_workspace_size(ctypes.byref(p), ctypes.byref(rg), ctypes.byref(mn),
+                                              ctypes.byref(rec)), "dsa_gated_delta_workspace_size")
+    return mn.value, rec.value
+
+
+def dsa_gated_delta_prefill(delta: DeltaShape, rg: Ragged, q, k, v, g, beta, out, state_in=None,
+                            state_out=None, state_index=None, workspace=None, ws_bytes=None,
+                            stream=None):
+    """The gated delta rule over a ragged batch: out [total_q, Hv, d], states [slots, Hv, dv, dk]."""
+    where, device = "dsa_gated_delta_prefill", _device(stream)
+    p, args = _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out,
+                          state_index, device)
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is not None and workspace.get_device() != device:
+        _bad(where, f"workspace on {workspace.device}, not cuda:{device}")
+    _check(lib.dsa_gated_delta_prefill(ctypes.byref(p), ctypes.byref(rg), *args, _ptr(workspace),
+                                       ws_bytes, _stream(stream)), where)
+
+
+def dsa_gated_delta_decode(delta: DeltaShape, rg: Ragged, q, k, v, g, beta, out, state_in=None,
+                           state_out=None, state_index=None, stream=None):
+    """dsa_gated_delta_prefill for at most one token per sequence, without a workspace."""
+    where, device = "dsa_gated_delta_decode", _device(stream)
+    p, args = _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out,
+                          state_index, device)
+    _check(lib.dsa_gated_delta_decode(ctypes.byref(p), ctypes.byref(rg), *args, _stream(stream)),
+           where)
 
 
 def dsa_device_status(clear: bool = True, stream=None) -> int:

@@ -38,7 +38,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
-    cmd = [nvcc, *NVCC_FLAGS, "-I" + INCLUDE, "-o", LIB + ".tmp", os.path.join(CSRC, "dsa.cu")]
+    cmd = [nvcc, *NVCC_FLAGS, "--threads", "2", "-I" + INCLUDE, "-o", LIB + ".tmp",
+           os.path.join(CSRC, "dsa.cu"), os.path.join(CSRC, "hybrid.cu")]
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)

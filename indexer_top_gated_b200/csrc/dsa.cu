@@ -1,7 +1,8 @@
 // dsa.cu - C ABI of the gated Indexer + Top-K sparse-attention layer (include/dsa.h):
 // argument validation, launch configuration, TMA tensor maps, the fused prefill and
 // decode drivers, per-stage timing and the device status word.  All kernels live in
-// the headers included here, so the library is one translation unit.
+// the headers included here; the entry points around the layer (rotary append, short
+// convolution, gated delta rule) are in hybrid.cu.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -14,6 +15,7 @@
 
 #include "dsa.h"
 #include "common.cuh"
+#include "hybrid.h"
 #include "idx_cand.cuh"
 #include "idx_scores.cuh"
 #include "sparse_attn.cuh"
@@ -181,6 +183,7 @@ dsa_status device_setup(DeviceState** out) {
     e = e ? e : allow_smem(sparse_attn_kernel<2, 1, kAddrUnits32>, attn_smem_bytes());
     e = e ? e : allow_smem(sparse_attn_kernel<1, 2, kAddrUnits32>, attn_smem_bytes());
     e = e ? e : allow_smem(sparse_attn_kernel<2, 2, kAddrUnits32>, attn_smem_bytes());
+    e = e ? e : hybrid_allow_smem();
     if (e != cudaSuccess) return DSA_ERR_CUDA;
     if (!g_encode) {
       void* fn = nullptr;
@@ -197,6 +200,19 @@ dsa_status device_setup(DeviceState** out) {
   *out = &d;
   return DSA_OK;
 }
+
+}  // namespace
+
+dsa_status hybrid_device(int* num_sms) {
+  DeviceState* dev = nullptr;
+  const dsa_status s = device_setup(&dev);
+  if (s == DSA_OK) *num_sms = dev->num_sms;
+  return s;
+}
+
+void count_launches(int n) { t_launches += n; }
+
+namespace {
 
 // ---------------------------------------------------------------- validation
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
