@@ -28,8 +28,6 @@
 // bf16: P enters rounded once and U with two pieces, an error no larger than that rounding's.
 #pragma once
 
-#include <type_traits>
-
 #include "common.cuh"
 
 namespace dsa {
@@ -203,21 +201,31 @@ DSA_DEV void split_pair(float x, float y, uint32_t (&p)[N]) {
 
 // ------------------------------------------------------------------ chunked form: T and P
 //
-// One CTA per (chunk, value head): K K^T by its four warps, then two warps invert I + A (a
-// column of the inverse per thread, forward substitution in fp32 with the column in registers
-// and the rows of A broadcast from shared memory) while the other two form P.
+// One CTA per (chunk, value head).  Each of its four warps forms 16 rows of K K^T and Q K^T up
+// to the diagonal (they share K's operands and the decays); then I + A is inverted in place, in
+// fp32: its 16 x 16 diagonal blocks by forward substitution, and the blocks below by
+//   [T1 0; -T2 A21 T1, T2], twice, 16 -> 32 -> 64.
+// Written as loops rather than one unrolled substitution over 64 rows: that was bound by
+// instruction fetch.
 constexpr int kPrepThreads = 128;
-constexpr int kPrepALd = 68;  // floats per row of A: 16-byte rows, and pairs of rows on other banks
+constexpr int kPrepLd = 68;  // floats per row of A: 16-byte rows, eight rows on distinct banks
+constexpr int kPrepLdM = 36;
 
 struct PrepSmem {
-  unsigned char k[kDeltaTile];
-  unsigned char q[kDeltaTile];
-  float A[kDeltaChunk * kPrepALd];
-  double G[kDeltaChunk];
+  union {
+    struct {
+      unsigned char k[kDeltaTile], q[kDeltaTile];
+    };
+    struct {  // once the products are in registers
+      float A[kDeltaChunk * kPrepLd];
+      float M[32 * kPrepLdM];
+    };
+  };
+  float2 G[kDeltaChunk];  // running sum of g, high and low part
   float ink[kDeltaChunk], inq[kDeltaChunk], beta[kDeltaChunk];
 };
 
-__global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const DeltaArgs a) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -233,24 +241,29 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaArg
   }
   const int64_t first = __ldg(a.q_offsets + lo), end = __ldg(a.q_offsets + lo + 1);
   const int64_t row0 = first + (slot - delta_first_slot(a, lo)) * kDeltaChunk;
-  const int64_t len = end - first;
-  if (len < a.min_len || row0 >= end) return;
+  if (end - first < a.min_len || row0 >= end) return;
   const int valid = (int)(end - row0 < kDeltaChunk ? end - row0 : kDeltaChunk);
   const int hk = h / (a.hv / a.hk);
 
   const uint32_t sk = smem_u32(sm.k), sq = smem_u32(sm.q);
+  {
+    const int r0 = tid >> 4, c = tid & 15;
+    const __nv_bfloat16* k = a.k + row0 * a.k_stride + hk * kDeltaDim + c * 8;
+    const __nv_bfloat16* q = a.q + row0 * a.q_stride + hk * kDeltaDim + c * 8;
 #pragma unroll
-  for (int i = 0; i < kDeltaTile / 16 / kPrepThreads; ++i) {
-    const int at = tid + i * kPrepThreads, r = at >> 4, c = at & 15;
-    const bool in = r < valid;
-    const int64_t row = row0 + (in ? r : 0);
-    cp_async_16(sk + swz256(r, c), a.k + row * a.k_stride + hk * kDeltaDim + c * 8, in ? 16 : 0);
-    cp_async_16(sq + swz256(r, c), a.q + row * a.q_stride + hk * kDeltaDim + c * 8, in ? 16 : 0);
+    for (int i = 0; i < kDeltaTile / 16 / kPrepThreads; ++i) {
+      const int r = r0 + i * (kPrepThreads / 16);
+      const bool in = r < valid;
+      const int64_t rr = in ? r : 0;
+      cp_async_16(sk + swz256(r, c), k + rr * a.k_stride, in ? 16 : 0);
+      cp_async_16(sq + swz256(r, c), q + rr * a.q_stride, in ? 16 : 0);
+    }
   }
   cp_async_commit();
   if (warp == 0) {
-    // running sum of g, two tokens a lane.  -inf (alpha = 0) becomes a finite decay that is 0
-    // all the same, so that differences of sums behind it stay numbers.
+    // running sum of g, two tokens a lane, in fp64 and then as a pair of fp32.  -inf (alpha = 0)
+    // becomes a finite decay that is 0 all the same, so that differences of sums behind it stay
+    // numbers.
     double x[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -265,8 +278,11 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaArg
       const double up = __shfl_up_sync(~0u, sum, m);
       if (lane >= m) sum += up;
     }
-    sm.G[lane * 2] = sum - own + x[0];
-    sm.G[lane * 2 + 1] = sum;
+    const double first_of_two = sum - own + x[0];
+    float f = (float)first_of_two;
+    sm.G[lane * 2] = make_float2(f, (float)(first_of_two - f));
+    f = (float)sum;
+    sm.G[lane * 2 + 1] = make_float2(f, (float)(sum - f));
   } else if (warp == 1) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -281,7 +297,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaArg
     const unsigned char* tile = tid < 64 ? sm.k : sm.q;
     float ss = 0.f;
     if (a.norm) {
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < 16; ++c) {
         const uint4 x = *reinterpret_cast<const uint4*>(tile + swz256(r, c));
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -294,168 +310,226 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const DeltaArg
     }
     (tid < 64 ? sm.ink : sm.inq)[r] = a.norm ? 1.f / sqrtf(ss + a.eps) : 1.f;
   }
-  __syncthreads();
+
+  // rows of 16 tokens (tile mt) of K K^T and Q K^T, columns up to the diagonal tile.  The tiles
+  // turn with the item, so that the longest is not always on the same scheduler.
+  const int mi = lane >> 3, mr = lane & 7;
+  const int mt = (warp + (int)(item & 3)) & 3;
+  float kk[8][4], qk[8][4];
+#pragma unroll
+  for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kk[nt][i] = qk[nt][i] = 0.f;
+#pragma unroll 2
+  for (int kt = 0; kt < 8; ++kt) {
+    uint32_t fk[4], fq[4];
+    ldmatrix_x4(sk + swz256(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fk);
+    ldmatrix_x4(sq + swz256(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fq);
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      if (np <= mt) {
+        uint32_t fb[4];
+        ldmatrix_x4(sk + swz256(np * 16 + (mi >> 1) * 8 + mr, kt * 2 + (mi & 1)), fb);
+        mma_bf16_16816(kk[np * 2], fk, fb[0], fb[1]);
+        mma_bf16_16816(kk[np * 2 + 1], fk, fb[2], fb[3]);
+        mma_bf16_16816(qk[np * 2], fq, fb[0], fb[1]);
+        mma_bf16_16816(qk[np * 2 + 1], fq, fb[2], fb[3]);
+      }
+    }
+  }
+  __syncthreads();  // the norms are there; K's and Q's tiles are free
 
   unsigned char* dst = a.ws + item * kDeltaItemBytes;
   if (tid < 64) {
     float* scal = reinterpret_cast<float*>(dst + kDeltaScal);
-    const float eg = expf((float)sm.G[tid]);
+    const float2 g = sm.G[tid], ge = sm.G[63];
+    const float eg = expf(g.x + g.y);
     scal[tid] = eg * sm.ink[tid];
-    scal[64 + tid] = expf((float)(sm.G[63] - sm.G[tid])) * sm.ink[tid];
+    scal[64 + tid] = expf((ge.x - g.x) + (ge.y - g.y)) * sm.ink[tid];
     scal[128 + tid] = a.scale * eg * sm.inq[tid];
-    if (tid == 0) scal[192] = expf((float)sm.G[63]);
+    if (tid == 0) scal[192] = expf(ge.x + ge.y);
   }
-
-  // rows of 16 tokens (tile mt) of X K^T, columns up to the diagonal tile
-  const int mi = lane >> 3, mr = lane & 7;
-  auto rows_x_k = [&](uint32_t xs, int mt, float (&acc)[8][4]) {
+  float2 gi[2];
+  float fa[2], fp[2];
+  int row[2];
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
+  for (int half = 0; half < 2; ++half) {
+    const int i = mt * 16 + (lane >> 2) + half * 8;
+    row[half] = i;
+    gi[half] = sm.G[i];
+    fa[half] = sm.beta[i] * sm.ink[i];
+    fp[half] = a.scale * sm.inq[i];
+  }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-#pragma unroll
-    for (int kt = 0; kt < 8; ++kt) {
-      uint32_t fa[4];
-      ldmatrix_x4(xs + swz256(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fa);
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        if (np > mt) break;
-        uint32_t fb[4];
-        ldmatrix_x4(sk + swz256(np * 16 + (mi >> 1) * 8 + mr, kt * 2 + (mi & 1)), fb);
-        mma_bf16_16816(acc[np * 2], fa, fb[0], fb[1]);
-        mma_bf16_16816(acc[np * 2 + 1], fa, fb[2], fb[3]);
-      }
-    }
-  };
-  // the roles turn with the item: the inversion's long warp is not always on the same scheduler
-  const int role = (warp + (int)(item & 3)) & 3;
-  {
-    float acc[8][4];
-    const int mt = role;
-    rows_x_k(sk, mt, acc);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      if (nt >= 2 * (mt + 1)) break;
+  for (int nt = 0; nt < 8; ++nt) {
+    if (nt < 2 * (mt + 1)) {
+      const int j = nt * 8 + (lane & 3) * 2;
+      const float4 gj = *reinterpret_cast<const float4*>(sm.G + j);
+      const float2 ik = *reinterpret_cast<const float2*>(sm.ink + j);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int i = mt * 16 + (lane >> 2) + half * 8, j = nt * 8 + (lane & 3) * 2;
+        const int i = row[half];
+        // e^(G_i - G_j): the high parts cancel exactly where it matters
+        const float d0 = j <= i ? __expf((gi[half].x - gj.x) + (gi[half].y - gj.y)) * ik.x : 0.f;
+        const float d1 = j < i ? __expf((gi[half].x - gj.z) + (gi[half].y - gj.w)) * ik.y : 0.f;
         float2 x;
-        x.x = j < i ? sm.beta[i] * sm.ink[i] * sm.ink[j] * expf((float)(sm.G[i] - sm.G[j])) *
-                          acc[nt][half * 2]
-                    : 0.f;
-        x.y = j + 1 < i ? sm.beta[i] * sm.ink[i] * sm.ink[j + 1] *
-                              expf((float)(sm.G[i] - sm.G[j + 1])) * acc[nt][half * 2 + 1]
-                        : 0.f;
-        *reinterpret_cast<float2*>(sm.A + i * kPrepALd + j) = x;
+        x.x = j < i ? fa[half] * d0 * kk[nt][half * 2] : 0.f;
+        x.y = j + 1 < i ? fa[half] * d1 * kk[nt][half * 2 + 1] : 0.f;
+        *reinterpret_cast<float2*>(sm.A + i * kPrepLd + j) = x;
+        *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + swz128(i, nt) + (lane & 3) * 4) =
+            pack_bf16x2(j <= i ? fp[half] * d0 * qk[nt][half * 2] : 0.f,
+                        j < i ? fp[half] * d1 * qk[nt][half * 2 + 1] : 0.f);
       }
+    } else if (nt < 2 * ((mt | 1) + 1)) {  // above the diagonal inside a 32 x 32 block
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        *reinterpret_cast<float2*>(sm.A + row[half] * kPrepLd + nt * 8 + (lane & 3) * 2) =
+            make_float2(0.f, 0.f);
+    }
+  }
+  __syncwarp();  // a warp's own rows hold its diagonal block
+  {
+    // column c of the block's inverse: x_i = [i == c] - sum_{m < i} A_im x_m
+    const int c = lane & 15;
+    float* A = sm.A + mt * 16 * kPrepLd + mt * 16;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int m = 0; m < i; m += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(A + i * kPrepLd + m);
+        s0 = fmaf(v.x, x[m], s0);
+        s1 = fmaf(v.y, x[m + 1], s1);
+        s0 = fmaf(v.z, x[m + 2], s0);
+        s1 = fmaf(v.w, x[m + 3], s1);
+      }
+      x[i] = (i == c ? 1.f : 0.f) - (s0 + s1);
+    }
+    __syncwarp();
+    if (lane < 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) A[i * kPrepLd + c] = x[i];
     }
   }
   __syncthreads();
-  if (role >= 2) {
-    // column j of T: x_i = [i == j] - sum_{m < i} A_im x_m
-    const int j = (role - 2) * 32 + lane;
-    const int base = (role - 2) * 32;
-    float x[kDeltaChunk];
-    auto solve = [&](auto from) {
-      constexpr int F = decltype(from)::value;
+  {  // 16 -> 32: two pairs of blocks, four values a thread
+    const int p = tid >> 6, r = (tid & 63) >> 2, c = (tid & 3) * 4;
+    float* T1 = sm.A + p * 32 * (kPrepLd + 1);
+    float* A21 = T1 + 16 * kPrepLd;
+    const float* T2 = A21 + 16;
+    float* M = sm.M + p * 16 * kPrepLdM;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < 16; ++k) {
+      const float x = A21[r * kPrepLd + k];
+      const float4 y = *reinterpret_cast<const float4*>(T1 + k * kPrepLd + c);
+      acc.x = fmaf(x, y.x, acc.x), acc.y = fmaf(x, y.y, acc.y);
+      acc.z = fmaf(x, y.z, acc.z), acc.w = fmaf(x, y.w, acc.w);
+    }
+    *reinterpret_cast<float4*>(M + r * kPrepLdM + c) = acc;
+    __syncthreads();
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < 16; ++k) {
+      const float x = T2[r * kPrepLd + k];
+      const float4 y = *reinterpret_cast<const float4*>(M + k * kPrepLdM + c);
+      acc.x = fmaf(-x, y.x, acc.x), acc.y = fmaf(-x, y.y, acc.y);
+      acc.z = fmaf(-x, y.z, acc.z), acc.w = fmaf(-x, y.w, acc.w);
+    }
+    *reinterpret_cast<float4*>(A21 + r * kPrepLd + c) = acc;
+  }
+  __syncthreads();
+  {  // 32 -> 64: eight values a thread
+    const int r = tid >> 2, c = (tid & 3) * 8;
+    float* A21 = sm.A + 32 * kPrepLd;
+    const float* T2 = A21 + 32;
+    float acc[8];
+    auto product = [&](const float* x, const float* y, int ldy) {
 #pragma unroll
-      for (int i = F; i < kDeltaChunk; ++i) x[i] = 0.f;
-#pragma unroll
-      for (int i = F; i < kDeltaChunk; ++i) {
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-        for (int m = F; m < i; m += 4) {
-          const float4 row = *reinterpret_cast<const float4*>(sm.A + i * kPrepALd + m);
-          s0 = fmaf(row.x, x[m], s0);
-          s1 = fmaf(row.y, x[m + 1], s1);
-          s2 = fmaf(row.z, x[m + 2], s2);
-          s3 = fmaf(row.w, x[m + 3], s3);
-        }
-        x[i] = (i == j ? 1.f : 0.f) - ((s0 + s1) + (s2 + s3));
-      }
-      const float bj = sm.beta[j];
-#pragma unroll
-      for (int i = F; i < kDeltaChunk; ++i) {
-        if ((i >> 4) < (j >> 4)) continue;
-        float y = x[i] * bj;
-        unsigned char* at = dst + swz128(i, j >> 3) + (j & 7) * 2;
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const __nv_bfloat16 piece = __float2bfloat16_rn(y);
-          *reinterpret_cast<__nv_bfloat16*>(at + p * kDeltaMat) = piece;
-          y -= __bfloat162float(piece);
-        }
+      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < 32; ++k) {
+        const float f = x[r * kPrepLd + k];
+        const float4 u = *reinterpret_cast<const float4*>(y + k * ldy + c);
+        const float4 v = *reinterpret_cast<const float4*>(y + k * ldy + c + 4);
+        acc[0] = fmaf(f, u.x, acc[0]), acc[1] = fmaf(f, u.y, acc[1]);
+        acc[2] = fmaf(f, u.z, acc[2]), acc[3] = fmaf(f, u.w, acc[3]);
+        acc[4] = fmaf(f, v.x, acc[4]), acc[5] = fmaf(f, v.y, acc[5]);
+        acc[6] = fmaf(f, v.z, acc[6]), acc[7] = fmaf(f, v.w, acc[7]);
       }
     };
-    if (base == 0) solve(std::integral_constant<int, 0>{});
-    else solve(std::integral_constant<int, 32>{});
-  } else {
-#pragma unroll 1
-    for (int w = 0; w < 2; ++w) {
-      const int mt = w == 0 ? role : 3 - role;
-      float acc[8][4];
-      rows_x_k(sq, mt, acc);
+    product(A21, sm.A, kPrepLd);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        if (nt >= 2 * (mt + 1)) break;
+    for (int i = 0; i < 8; i += 4)
+      *reinterpret_cast<float4*>(sm.M + r * kPrepLdM + c + i) =
+          make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    __syncthreads();
+    product(T2, sm.M, kPrepLdM);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int i = mt * 16 + (lane >> 2) + half * 8, j = nt * 8 + (lane & 3) * 2;
-          const float f = a.scale * sm.inq[i];
-          const float x = j <= i ? f * sm.ink[j] * expf((float)(sm.G[i] - sm.G[j])) *
-                                       acc[nt][half * 2]
-                                 : 0.f;
-          const float y = j + 1 <= i ? f * sm.ink[j + 1] * expf((float)(sm.G[i] - sm.G[j + 1])) *
-                                           acc[nt][half * 2 + 1]
-                                     : 0.f;
-          *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + swz128(i, nt) + (lane & 3) * 4) =
-              pack_bf16x2(x, y);
-        }
-      }
+    for (int i = 0; i < 8; i += 4)
+      *reinterpret_cast<float4*>(A21 + r * kPrepLd + c + i) =
+          make_float4(-acc[i], -acc[i + 1], -acc[i + 2], -acc[i + 3]);
+  }
+  __syncthreads();
+  // T diag(beta) in three pieces, eight columns at a time
+#pragma unroll
+  for (int n = 0; n < kDeltaChunk * 8 / kPrepThreads; ++n) {
+    const int at = tid + n * kPrepThreads, i = at >> 3, c = at & 7;
+    if (c >= 2 * ((i >> 4) + 1)) continue;
+    uint32_t p[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = *reinterpret_cast<const float2*>(sm.A + i * kPrepLd + c * 8 + e * 2);
+      const float2 w = *reinterpret_cast<const float2*>(sm.beta + c * 8 + e * 2);
+      split_pair<3>(t.x * w.x, t.y * w.y, p[e]);
     }
+#pragma unroll
+    for (int m = 0; m < 3; ++m)
+      *reinterpret_cast<uint4*>(dst + m * kDeltaMat + swz128(i, c)) =
+          make_uint4(p[0][m], p[1][m], p[2][m], p[3][m]);
   }
 }
 
 // ------------------------------------------------------------------ chunked form: the scan
 //
-// A CTA walks one sequence's chunks for one head and NV of its 128 value columns.  Products are
-// taken transposed, with 16 value columns as the rows of the tensor-core tile:
+// A CTA walks one sequence's chunks for one head and kScanNV of its 128 value columns.  Products
+// are taken transposed, with 16 value columns as the rows of the tensor-core tile:
 //   R^T = S K^T, QS^T = S Q^T, U^T = X^T T^T, S += U'^T K, O^T = QS^T + U^T P^T
 // so that an accumulator tile is, register for register, the next product's left operand, and
-// the right operands (K, Q, T, P) come from shared memory by ldmatrix.  Two warps share 16 value
-// columns.  Each owns 64 of the key columns of S (32 registers) and two of the four 16-token
-// tiles, {0, 3} or {1, 2} (equal work in the triangular products); three exchanges through
-// shared memory a chunk bring the halves of R and QS together and hand X and U around.
-template <int NV>
-struct ScanGeo {
-  static constexpr int kPairs = NV / 16;
-  static constexpr int kThreads = kPairs * 64;
-  static constexpr int kVBytes = kDeltaChunk * NV * 2;
-  // one chunk's operands: K, Q, the workspace item, V
-  static constexpr int kItemOff = 2 * kDeltaTile;
-  static constexpr int kVOff = kItemOff + kDeltaItemBytes;
-  static constexpr int kStage = kVOff + kVBytes;
-  // exchange area of a pair: halves of R and QS (8 KB), later U and U' (10 KB); X (6 KB)
-  static constexpr int kExch = 10240 + 6144;
-  static constexpr int kSmem = 2 * kStage + kPairs * kExch;
-};
+// the right operands (K, Q, T, P) come from shared memory by ldmatrix.  Four warps share 16
+// value columns.  Two carry the chain R -> X -> U -> S: each owns 64 of the key columns of S (32
+// registers) and two of the four 16-token tiles, {0, 3} or {1, 2} (equal work in the triangular
+// products), and three exchanges through shared memory a chunk bring the halves of R together
+// and hand X and U around.  The other two, off the chain, load the next chunk and compute O.
+// What bounds it: the chain's latency (220 tensor instructions a warp and chunk, which depend on
+// one another in four stages); the tensor pipe, which the output warps fill in the gaps, is the
+// next limit (304 a scheduler and chunk).  So accumulators alternate, eight or six between two
+// uses of one, and operands are fetched one step ahead.
+constexpr int kScanNV = 32;
+constexpr int kScanPairs = kScanNV / 16;
+constexpr int kScanThreads = kScanPairs * 128;
+constexpr int kScanLoaders = kScanPairs * 64;  // the output warps' threads
+// one chunk's operands: K, Q, the workspace item, V
+constexpr int kScanItem = 2 * kDeltaTile;
+constexpr int kScanV = kScanItem + kDeltaItemBytes;
+constexpr int kScanStage = kScanV + kDeltaChunk * kScanNV * 2;
+// exchange areas of 16 value columns, 512 bytes (a fragment of a warp) each unit: S [8 key tiles]
+// [2 pieces], R [2 warps][4], X [4 token tiles][3 pieces], U and U' [4 token tiles][2 + 3]
+constexpr int kExS = 0, kExR = kExS + 16 * 512, kExX = kExR + 8 * 512, kExU = kExX + 12 * 512;
+constexpr int kScanExch = kExU + 20 * 512;
+constexpr int kScanSmem = 2 * kScanStage + kScanPairs * kScanExch;
 
-// 16-byte unit of value columns 8u .. 8u+7 of token r in the V tile
-template <int NV>
-DSA_DEV uint32_t swzv(int r, int u) {
-  if (NV == 16) return r * 32 + ((u ^ ((r >> 2) & 1)) << 4);
-  if (NV == 32) return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
-  return r * 128 + ((u ^ (r & 7)) << 4);
-}
+// 16-byte unit u (value columns 8u .. 8u+7) of token r in the V tile, rows of 64 bytes
+DSA_DEV uint32_t swz64(int r, int u) { return r * 64 + ((u ^ ((r >> 1) & 3)) << 4); }
 
-template <int NV>
-DSA_DEV void scan_load(const DeltaArgs& a, uint32_t stage, int64_t row0, int valid, int h, int hk,
-                       int dv0, const unsigned char* item) {
-  using Geo = ScanGeo<NV>;
-  const int tid = threadIdx.x;
+DSA_DEV void scan_load(const DeltaArgs& a, int tid, uint32_t stage, int64_t row0, int valid, int h,
+                       int hk, int dv0, const unsigned char* item) {
 #pragma unroll
-  for (int i = 0; i < kDeltaTile / 16 / Geo::kThreads; ++i) {
-    const int at = tid + i * Geo::kThreads, r = at >> 4, c = at & 15;
+  for (int i = 0; i < kDeltaTile / 16 / kScanLoaders; ++i) {
+    const int at = tid + i * kScanLoaders, r = at >> 4, c = at & 15;
     const bool in = r < valid;
     const int64_t row = row0 + (in ? r : 0);
     cp_async_16(stage + swz256(r, c), a.k + row * a.k_stride + hk * kDeltaDim + c * 8, in ? 16 : 0);
@@ -464,20 +538,24 @@ DSA_DEV void scan_load(const DeltaArgs& a, uint32_t stage, int64_t row0, int val
   }
   // T and P: the units of the 16 x 16 blocks up to the diagonal
 #pragma unroll
-  for (int i = 0; i < 4 * kDeltaMat / 16 / Geo::kThreads; ++i) {
-    const int at = tid + i * Geo::kThreads, r = (at >> 3) & 63, c = (at & 7) ^ (r & 7);
-    if (c < 2 * ((r >> 4) + 1))
-      cp_async_16(stage + Geo::kItemOff + at * 16, item + at * 16, 16);
+  for (int i = 0; i < 4 * kDeltaMat / 16 / kScanLoaders; ++i) {
+    const int at = tid + i * kScanLoaders, r = (at >> 3) & 63, c = (at & 7) ^ (r & 7);
+    if (c < 2 * ((r >> 4) + 1)) cp_async_16(stage + kScanItem + at * 16, item + at * 16, 16);
   }
-  if (tid < 52) cp_async_16(stage + Geo::kItemOff + kDeltaScal + tid * 16, item + kDeltaScal + tid * 16, 16);
+  if (tid < 52)
+    cp_async_16(stage + kScanItem + kDeltaScal + tid * 16, item + kDeltaScal + tid * 16, 16);
 #pragma unroll
-  for (int i = 0; i < Geo::kVBytes / 16 / Geo::kThreads; ++i) {
-    const int at = tid + i * Geo::kThreads, r = at / (NV / 8), c = at % (NV / 8);
+  for (int i = 0; i < kDeltaChunk * kScanNV / 8 / kScanLoaders; ++i) {
+    const int at = tid + i * kScanLoaders, r = at >> 2, c = at & 3;
     const bool in = r < valid;
     const int64_t row = row0 + (in ? r : 0);
-    cp_async_16(stage + Geo::kVOff + swzv<NV>(r, c),
+    cp_async_16(stage + kScanV + swz64(r, c),
                 a.v + row * a.v_stride + (int64_t)h * kDeltaDim + dv0 + c * 8, in ? 16 : 0);
   }
+}
+
+DSA_DEV void named_barrier_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 DSA_DEV void st_frag(unsigned char* p, const uint32_t (&f)[4]) {
@@ -506,278 +584,230 @@ DSA_DEV void split_frag(const float (&x)[4], const float (&y)[4], uint32_t (&f)[
   for (int i = 0; i < N; ++i) f[i][3] = p[i];
 }
 
-template <int NV>
-__global__ void __launch_bounds__(ScanGeo<NV>::kThreads) delta_scan_kernel(const DeltaArgs a) {
-  using Geo = ScanGeo<NV>;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pair = warp >> 1, w = warp & 1;
-  constexpr int kParts = kDeltaDim / NV;
-  const int part = blockIdx.x % kParts;
-  const int hl = (blockIdx.x / kParts) % a.heads;
-  const int b = blockIdx.x / (kParts * a.heads);
-  const int h = a.head0 + hl, hk = h / (a.hv / a.hk);
-  const int64_t first = __ldg(a.q_offsets + b);
-  const int len = (int)(__ldg(a.q_offsets + b + 1) - first);
-  if (len < a.min_len) return;
-  const int64_t slot = delta_slot(a, b);
-  const int dvc = part * NV;          // the CTA's first value column
-  const int dv0 = dvc + pair * 16;    // the pair's
-  const int n_chunks = (len + kDeltaChunk - 1) / kDeltaChunk;
-  const unsigned char* items =
-      a.ws + (delta_first_slot(a, b) * a.heads + hl) * (int64_t)kDeltaItemBytes;
-  const int64_t item_step = (int64_t)a.heads * kDeltaItemBytes;
+// The five (token tile, key token tile) blocks of a triangular product that warp w of a pair
+// computes, its tiles being 0 and 3 or 1 and 2.  Both warps run the same code (twice the code
+// was bound by instruction fetch): blocks 0 .. 3 are (second, 0), (first, 0), (second, 1),
+// (second, 2), and block 4 is (3, 3) of the one or (1, 1) of the other.
+DSA_DEV int tri_tile(int w, int i) { return i ? 3 - w : w; }
+DSA_DEV constexpr int tri_own(int b) { return b == 1 ? 0 : 1; }
+DSA_DEV constexpr int tri_kt(int b) { return b < 2 ? 0 : b - 1; }
 
-  unsigned char* ex1 = smem + 2 * Geo::kStage + pair * Geo::kExch;  // R and QS halves, then U
-  unsigned char* ex2 = ex1 + 10240;                                 // X
-  const uint32_t stage0 = smem_u32(smem);
-  const int mi = lane >> 3, mr = lane & 7;
+struct ScanPlace {
+  int64_t first, slot;
+  int len, h, hk, dvc;  // dvc: the CTA's first value column
+  const unsigned char* items;
+  int64_t item_step;
+};
+
+// The chain: warp w of the pair whose exchange area is ex.
+DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* smem,
+                        unsigned char* ex, int pair, int w) {
+  const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
+  const int dv0 = at.dvc + pair * 16;
+  const int bar = 1 + 3 * pair;
+  const int tile[2] = {tri_tile(w, 0), tri_tile(w, 1)};
+  const int their[2] = {tri_tile(1 - w, 0), tri_tile(1 - w, 1)};
+  const int kt4 = w ? 1 : 3;
+  ex += lane * 16;
 
   // S^T of this warp: rows dv0 + lane/4 (+8), columns 64 w + 8 n + 2 (lane % 4) (+1)
   float s[8][4];
-  const int64_t soff = ((slot * a.hv + h) * kDeltaDim + dv0 + (lane >> 2)) * kDeltaDim + w * 64 +
-                       (lane & 3) * 2;
+  const int64_t soff =
+      ((at.slot * a.hv + at.h) * kDeltaDim + dv0 + (lane >> 2)) * kDeltaDim + w * 64 + (lane & 3) * 2;
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     float2 x = make_float2(0.f, 0.f), y = x;
-    if (a.state_in && slot >= 0) {
+    if (a.state_in && at.slot >= 0) {
       x = *reinterpret_cast<const float2*>(a.state_in + soff + n * 8);
       y = *reinterpret_cast<const float2*>(a.state_in + soff + 8 * kDeltaDim + n * 8);
     }
     s[n][0] = x.x, s[n][1] = x.y, s[n][2] = y.x, s[n][3] = y.y;
   }
 
-  scan_load<NV>(a, stage0, first, len < kDeltaChunk ? len : kDeltaChunk, h, hk, dvc, items);
-  cp_async_commit();
-
+  const uint32_t stage0 = smem_u32(smem);
+  // byte offsets of this lane's ldmatrix rows: K's token tiles (own first), T's own tiles
+  const int rb = (mi >> 1) * 8 + mr;
+  uint32_t k_row[4], t_row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    k_row[i] = (tile[i] * 16 + rb) * 256;
+    k_row[2 + i] = (their[i] * 16 + rb) * 256;
+    t_row[i] = (tile[i] * 16 + rb) * 128;
+  }
+  const int n_chunks = (at.len + kDeltaChunk - 1) / kDeltaChunk;
 #pragma unroll 1
   for (int c = 0; c < n_chunks; ++c) {
-    const int64_t row0 = first + (int64_t)c * kDeltaChunk;
-    const int valid = len - c * kDeltaChunk < kDeltaChunk ? len - c * kDeltaChunk : kDeltaChunk;
-    cp_async_wait<0>();
     __syncthreads();  // chunk c is in place, and every warp is done with chunk c - 1
-    if (c + 1 < n_chunks) {
-      const int next = len - (c + 1) * kDeltaChunk;
-      scan_load<NV>(a, stage0 + ((c + 1) & 1) * Geo::kStage, row0 + kDeltaChunk,
-                    next < kDeltaChunk ? next : kDeltaChunk, h, hk, dvc,
-                    items + (c + 1) * item_step);
-      cp_async_commit();
-    }
-    const uint32_t sk = stage0 + (c & 1) * Geo::kStage, sq = sk + kDeltaTile;
-    const uint32_t st = sk + Geo::kItemOff, sp = st + 3 * kDeltaMat, sv = sk + Geo::kVOff;
-    const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * Geo::kStage + Geo::kItemOff +
+    const uint32_t sk = stage0 + (c & 1) * kScanStage;
+    const uint32_t st = sk + kScanItem, sv = sk + kScanV;
+    const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * kScanStage + kScanItem +
                                                        kDeltaScal);
 
-    // R^T = S K^T and QS^T = S Q^T over this warp's key columns, all tokens
-    float r[8][4], qs[8][4];
+    // R^T = S K^T over this warp's key columns: r[0..3] the own token tiles, r[4..7] the other's
+    float r[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[n][i] = qs[n][i] = 0.f;
+      for (int i = 0; i < 4; ++i) r[n][i] = 0.f;
+    uint32_t fb[2][4][4];
+    auto load_k = [&](int kt, uint32_t (&f)[4][4]) {
+      const uint32_t unit = ((w * 8 + kt * 2 + (mi & 1)) ^ mr) << 4;
+#pragma unroll
+      for (int np = 0; np < 4; ++np) ldmatrix_x4(sk + k_row[np] + unit, f[np]);
+    };
+    load_k(0, fb[0]);
+    uint32_t fs[4][2][4];
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-      uint32_t fa[2][4];
-      split_frag<2>(s[2 * kt], s[2 * kt + 1], fa);
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        const uint32_t at = swz256(np * 16 + (mi >> 1) * 8 + mr, w * 8 + kt * 2 + (mi & 1));
-        uint32_t fb[4], fq[4];
-        ldmatrix_x4(sk + at, fb);
-        ldmatrix_x4(sq + at, fq);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          mma_bf16_16816(r[2 * np], fa[p], fb[0], fb[1]);
-          mma_bf16_16816(r[2 * np + 1], fa[p], fb[2], fb[3]);
-          mma_bf16_16816(qs[2 * np], fa[p], fq[0], fq[1]);
-          mma_bf16_16816(qs[2 * np + 1], fa[p], fq[2], fq[3]);
-        }
-      }
+      split_frag<2>(s[2 * kt], s[2 * kt + 1], fs[kt]);
+      st_frag(ex + kExS + ((w * 4 + kt) * 2) * 512, fs[kt][0]);
+      st_frag(ex + kExS + ((w * 4 + kt) * 2 + 1) * 512, fs[kt][1]);
     }
-    // own token tiles: w = 0 has 0 and 3, w = 1 has 1 and 2
+    named_barrier_arrive(bar + 1, 128);  // the output warps may read S
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+      if (kt < 3) load_k(kt + 1, fb[(kt + 1) & 1]);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          const uint32_t(&f)[4] = fb[kt & 1][np];
+          mma_bf16_16816(r[2 * np], fs[kt][p], f[0], f[1]);
+          mma_bf16_16816(r[2 * np + 1], fs[kt][p], f[2], f[3]);
+        }
+    }
+    // the other warp's tokens to it, its share of the own tokens from it
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      *reinterpret_cast<float4*>(ex + kExR + (w * 4 + n) * 512) =
+          make_float4(r[4 + n][0], r[4 + n][1], r[4 + n][2], r[4 + n][3]);
+    uint32_t fv[2][4], ft[5][3][4];
+    float2 av[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int theirs = w ? (i ? 3 : 0) : (i ? 2 : 1);
+      ldmatrix_x4_trans(sv + swz64(tile[i] * 16 + rb, pair * 2 + (mi & 1)), fv[i]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        unsigned char* at = ex1 + w * 4096 + (i * 2 + e) * 1024 + lane * 16;
-        float4 x, y;
-        if (w) {
-          const int n = 2 * (i ? 3 : 0) + e;
-          x = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
-          y = make_float4(qs[n][0], qs[n][1], qs[n][2], qs[n][3]);
-        } else {
-          const int n = 2 * (i ? 2 : 1) + e;
-          x = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
-          y = make_float4(qs[n][0], qs[n][1], qs[n][2], qs[n][3]);
-        }
-        *reinterpret_cast<float4*>(at) = x;
-        *reinterpret_cast<float4*>(at + 512) = y;
-      }
-      (void)theirs;
+      for (int e = 0; e < 2; ++e)
+        av[i][e] = *reinterpret_cast<const float2*>(scal + tile[i] * 16 + e * 8 + (lane & 3) * 2);
     }
-    named_barrier(1 + pair, 64);
-    float ro[4][4], qo[4][4];  // own tiles' R and QS: [2 * tile + 8-token half]
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const unsigned char* at = ex1 + (1 - w) * 4096 + (i * 2 + e) * 1024 + lane * 16;
-        const float4 x = *reinterpret_cast<const float4*>(at);
-        const float4 y = *reinterpret_cast<const float4*>(at + 512);
-        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ro[2 * i + e][j] = (w ? r[2 * (i ? 2 : 1) + e][j] : r[2 * (i ? 3 : 0) + e][j]) + xs[j];
-          qo[2 * i + e][j] = (w ? qs[2 * (i ? 2 : 1) + e][j] : qs[2 * (i ? 3 : 0) + e][j]) + ys[j];
-        }
-      }
-
+    named_barrier(bar, 64);
     // X^T = V^T - R^T diag(a) of the own tokens, handed to both warps in three pieces
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tile = w ? (i ? 2 : 1) : (i ? 3 : 0);
-      uint32_t fv[4];
-      ldmatrix_x4_trans(sv + swzv<NV>(tile * 16 + (mi >> 1) * 8 + mr, pair * 2 + (mi & 1)), fv);
       float x[2][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float2 av = *reinterpret_cast<const float2*>(scal + tile * 16 + e * 8 + (lane & 3) * 2);
-        x[e][0] = bf16_lo(fv[2 * e]) - av.x * ro[2 * i + e][0];
-        x[e][1] = bf16_hi(fv[2 * e]) - av.y * ro[2 * i + e][1];
-        x[e][2] = bf16_lo(fv[2 * e + 1]) - av.x * ro[2 * i + e][2];
-        x[e][3] = bf16_hi(fv[2 * e + 1]) - av.y * ro[2 * i + e][3];
+        const float4 o =
+            *reinterpret_cast<const float4*>(ex + kExR + ((1 - w) * 4 + i * 2 + e) * 512);
+        const float(&own)[4] = r[2 * i + e];
+        x[e][0] = bf16_lo(fv[i][2 * e]) - av[i][e].x * (own[0] + o.x);
+        x[e][1] = bf16_hi(fv[i][2 * e]) - av[i][e].y * (own[1] + o.y);
+        x[e][2] = bf16_lo(fv[i][2 * e + 1]) - av[i][e].x * (own[2] + o.z);
+        x[e][3] = bf16_hi(fv[i][2 * e + 1]) - av[i][e].y * (own[3] + o.w);
       }
       uint32_t f[3][4];
       split_frag<3>(x[0], x[1], f);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) st_frag(ex2 + (tile * 3 + p) * 512 + lane * 16, f[p]);
+      for (int p = 0; p < 3; ++p) st_frag(ex + kExX + (tile[i] * 3 + p) * 512, f[p]);
     }
-    named_barrier(1 + pair, 64);
+#pragma unroll
+    for (int b = 0; b < 5; ++b) {
+      const uint32_t row = b < 4 ? t_row[tri_own(b)] : w ? t_row[0] : t_row[1];
+      const uint32_t unit = (((b < 4 ? tri_kt(b) : kt4) * 2 + (mi & 1)) ^ mr) << 4;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) ldmatrix_x4(st + p * kDeltaMat + row + unit, ft[b][p]);
+    }
+    named_barrier(bar, 64);
 
-    // U^T = X^T T^T of the own tokens
-    float u[4][4];
+    // U^T = X^T T^T of the own tokens; products of pieces below 2^-24 of the whole are left out.
+    // Accumulators: first tile; second tile, even and odd blocks; block 4
+    float u[4][2][4];
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[n][i] = 0.f;
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-      uint32_t f[3][4];
-      bool have = false;
+        for (int i = 0; i < 4; ++i) u[n][e][i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int tile = w ? (i ? 2 : 1) : (i ? 3 : 0);
-        if (kt > tile) continue;
-        if (!have) {
+    for (int px = 0; px < 3; ++px) {
+      uint32_t fx[4][4];
 #pragma unroll
-          for (int p = 0; p < 3; ++p) ld_frag(ex2 + (kt * 3 + p) * 512 + lane * 16, f[p]);
-          have = true;
+      for (int kt = 0; kt < 3; ++kt) ld_frag(ex + kExX + (kt * 3 + px) * 512, fx[kt]);
+      ld_frag(ex + kExX + (kt4 * 3 + px) * 512, fx[3]);
+#pragma unroll
+      for (int pt = 0; pt < 3 - px; ++pt)
+#pragma unroll
+        for (int b = 0; b < 5; ++b) {
+          float(&acc)[2][4] = u[b == 1 ? 0 : b == 4 ? 3 : b == 2 ? 2 : 1];
+          const uint32_t(&x)[4] = fx[b < 4 ? tri_kt(b) : 3];
+          mma_bf16_16816(acc[0], x, ft[b][pt][0], ft[b][pt][1]);
+          mma_bf16_16816(acc[1], x, ft[b][pt][2], ft[b][pt][3]);
         }
-#pragma unroll
-        for (int pt = 0; pt < 3; ++pt) {
-          uint32_t ft[4];
-          ldmatrix_x4(st + pt * kDeltaMat + swz128(tile * 16 + (mi >> 1) * 8 + mr, kt * 2 + (mi & 1)),
-                      ft);
-#pragma unroll
-          for (int px = 0; px < 3; ++px) {
-            if (px + pt > 2) continue;  // below 2^-24 of the product
-            mma_bf16_16816(u[2 * i], f[px], ft[0], ft[1]);
-            mma_bf16_16816(u[2 * i + 1], f[px], ft[2], ft[3]);
-          }
-        }
-      }
     }
     // U in two pieces for O, U' = U diag(t) in three for S
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tile = w ? (i ? 2 : 1) : (i ? 3 : 0);
-      uint32_t f2[2][4], f3[3][4];
-      split_frag<2>(u[2 * i], u[2 * i + 1], f2);
-      float y[2][4];
+      float x[2][4], y[2][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float2 tv =
-            *reinterpret_cast<const float2*>(scal + 64 + tile * 16 + e * 8 + (lane & 3) * 2);
-        y[e][0] = u[2 * i + e][0] * tv.x;
-        y[e][1] = u[2 * i + e][1] * tv.y;
-        y[e][2] = u[2 * i + e][2] * tv.x;
-        y[e][3] = u[2 * i + e][3] * tv.y;
+            *reinterpret_cast<const float2*>(scal + 64 + tile[i] * 16 + e * 8 + (lane & 3) * 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[e][j] = i ? u[1][e][j] + u[2][e][j] : u[0][e][j];
+          if ((i == 0) == (w == 1)) x[e][j] += u[3][e][j];
+        }
+        y[e][0] = x[e][0] * tv.x;
+        y[e][1] = x[e][1] * tv.y;
+        y[e][2] = x[e][2] * tv.x;
+        y[e][3] = x[e][3] * tv.y;
       }
+      uint32_t f2[2][4], f3[3][4];
       split_frag<3>(y[0], y[1], f3);
-      unsigned char* at = ex1 + tile * 5 * 512 + lane * 16;
+      split_frag<2>(x[0], x[1], f2);
+      unsigned char* to = ex + kExU + tile[i] * 5 * 512;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) st_frag(at + p * 512, f2[p]);
+      for (int p = 0; p < 2; ++p) st_frag(to + p * 512, f2[p]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) st_frag(at + (2 + p) * 512, f3[p]);
+      for (int p = 0; p < 3; ++p) st_frag(to + (2 + p) * 512, f3[p]);
     }
-    named_barrier(1 + pair, 64);
-
     // S = e^(G_C) S + U'^T K over this warp's key columns
+    auto load_kt = [&](int kt, uint32_t (&f)[4][4]) {
+#pragma unroll
+      for (int np = 0; np < 4; ++np)
+        ldmatrix_x4_trans(
+            sk + swz256(kt * 16 + (mi & 1) * 8 + mr, w * 8 + np * 2 + (mi >> 1)), f[np]);
+    };
+    load_kt(0, fb[0]);
     const float decay = scal[192];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[n][i] *= decay;
+    named_barrier(bar + 2, 128);
+    uint32_t fu[2][3][4];
+    auto load_u = [&](int kt, uint32_t (&f)[3][4]) {
+#pragma unroll
+      for (int p = 0; p < 3; ++p) ld_frag(ex + kExU + (kt * 5 + 2 + p) * 512, f[p]);
+    };
+    load_u(0, fu[0]);
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-      uint32_t f[3][4];
+      if (kt < 3) {
+        load_kt(kt + 1, fb[(kt + 1) & 1]);
+        load_u(kt + 1, fu[(kt + 1) & 1]);
+      }
 #pragma unroll
-      for (int p = 0; p < 3; ++p) ld_frag(ex1 + (kt * 5 + 2 + p) * 512 + lane * 16, f[p]);
+      for (int p = 0; p < 3; ++p)
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t fb[4];
-        ldmatrix_x4_trans(
-            sk + swz256(kt * 16 + (mi & 1) * 8 + mr, w * 8 + np * 2 + (mi >> 1)), fb);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          mma_bf16_16816(s[2 * np], f[p], fb[0], fb[1]);
-          mma_bf16_16816(s[2 * np + 1], f[p], fb[2], fb[3]);
+        for (int np = 0; np < 4; ++np) {
+          const uint32_t(&f)[4] = fb[kt & 1][np];
+          mma_bf16_16816(s[2 * np], fu[kt & 1][p], f[0], f[1]);
+          mma_bf16_16816(s[2 * np + 1], fu[kt & 1][p], f[2], f[3]);
         }
-      }
-    }
-
-    // O^T = QS^T diag(b) + U^T P^T of the own tokens
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int tile = w ? (i ? 2 : 1) : (i ? 3 : 0);
-      float o[2][4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 bv =
-            *reinterpret_cast<const float2*>(scal + 128 + tile * 16 + e * 8 + (lane & 3) * 2);
-        o[e][0] = qo[2 * i + e][0] * bv.x;
-        o[e][1] = qo[2 * i + e][1] * bv.y;
-        o[e][2] = qo[2 * i + e][2] * bv.x;
-        o[e][3] = qo[2 * i + e][3] * bv.y;
-      }
-#pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        if (kt > tile) continue;
-        uint32_t f[2][4], fp[4];
-        ldmatrix_x4(sp + swz128(tile * 16 + (mi >> 1) * 8 + mr, kt * 2 + (mi & 1)), fp);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          ld_frag(ex1 + (kt * 5 + p) * 512 + lane * 16, f[p]);
-          mma_bf16_16816(o[0], f[p], fp[0], fp[1]);
-          mma_bf16_16816(o[1], f[p], fp[2], fp[3]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t y0 = movmatrix_trans(pack_bf16x2(o[e][0], o[e][1]));
-        const uint32_t y1 = movmatrix_trans(pack_bf16x2(o[e][2], o[e][3]));
-        const int t = tile * 16 + e * 8 + (lane >> 2);
-        if (t < valid) {
-          uint32_t* at = reinterpret_cast<uint32_t*>(
-              a.out + ((row0 + t) * a.hv + h) * kDeltaDim + dv0 + (lane & 3) * 2);
-          at[0] = y0;
-          at[4] = y1;
-        }
-      }
     }
   }
-
-  if (a.state_out && slot >= 0) {
+  if (a.state_out && at.slot >= 0) {
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       *reinterpret_cast<float2*>(a.state_out + soff + n * 8) = make_float2(s[n][0], s[n][1]);
@@ -785,6 +815,152 @@ __global__ void __launch_bounds__(ScanGeo<NV>::kThreads) delta_scan_kernel(const
           make_float2(s[n][2], s[n][3]);
     }
   }
+}
+
+// The output warps: the next chunk's loads, then O^T = QS^T diag(b) + U^T P^T of the own tokens.
+DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char* smem,
+                         unsigned char* ex, int pair, int w) {
+  const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
+  const int loader = (pair * 2 + w) * 32 + lane;
+  const int dv0 = at.dvc + pair * 16;
+  const int bar = 1 + 3 * pair;
+  const int tile[2] = {tri_tile(w, 0), tri_tile(w, 1)};
+  const int kt4 = w ? 1 : 3;
+  ex += lane * 16;
+  const uint32_t stage0 = smem_u32(smem);
+  const int rb = (mi >> 1) * 8 + mr;
+  const int n_chunks = (at.len + kDeltaChunk - 1) / kDeltaChunk;
+
+  auto load = [&](int c) {
+    const int left = at.len - c * kDeltaChunk;
+    scan_load(a, loader, stage0 + (c & 1) * kScanStage, at.first + (int64_t)c * kDeltaChunk,
+              left < kDeltaChunk ? left : kDeltaChunk, at.h, at.hk, at.dvc,
+              at.items + c * at.item_step);
+    cp_async_commit();
+  };
+  // one copy of the loads' code: chunk c + 1 is asked for once chunk c has come
+#pragma unroll 1
+  for (int c = -1; c < n_chunks; ++c) {
+    if (c >= 0) {
+      cp_async_wait<0>();
+      __syncthreads();
+    }
+    if (c + 1 < n_chunks) load(c + 1);
+    if (c < 0) continue;
+    const uint32_t sq = stage0 + (c & 1) * kScanStage + kDeltaTile;
+    const uint32_t sp = sq + kDeltaTile + 3 * kDeltaMat;
+    const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * kScanStage + kScanItem +
+                                                       kDeltaScal);
+    float o[3][2][4];  // first tile, second tile, block 4
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][e][j] = 0.f;
+    uint32_t fq[2][2][4], fs[2][2][4];
+    auto load_q = [&](int kt, uint32_t (&f)[2][4]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        ldmatrix_x4(sq + swz256(tile[i] * 16 + rb, kt * 2 + (mi & 1)), f[i]);
+    };
+    auto load_s = [&](int kt, uint32_t (&f)[2][4]) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) ld_frag(ex + kExS + (kt * 2 + p) * 512, f[p]);
+    };
+    load_q(0, fq[0]);
+    named_barrier(bar + 1, 128);
+    load_s(0, fs[0]);
+#pragma unroll
+    for (int kt = 0; kt < 8; ++kt) {
+      if (kt < 7) {
+        load_q(kt + 1, fq[(kt + 1) & 1]);
+        load_s(kt + 1, fs[(kt + 1) & 1]);
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t(&f)[4] = fq[kt & 1][i];
+          mma_bf16_16816(o[i][0], fs[kt & 1][p], f[0], f[1]);
+          mma_bf16_16816(o[i][1], fs[kt & 1][p], f[2], f[3]);
+        }
+    }
+    uint32_t fp[5][4];
+#pragma unroll
+    for (int b = 0; b < 5; ++b) {
+      const int row = (b < 4 ? tile[tri_own(b)] : kt4) * 16 + rb;
+      ldmatrix_x4(sp + swz128(row, (b < 4 ? tri_kt(b) : kt4) * 2 + (mi & 1)), fp[b]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 bv =
+            *reinterpret_cast<const float2*>(scal + 128 + tile[i] * 16 + e * 8 + (lane & 3) * 2);
+        o[i][e][0] *= bv.x;
+        o[i][e][1] *= bv.y;
+        o[i][e][2] *= bv.x;
+        o[i][e][3] *= bv.y;
+      }
+    named_barrier(bar + 2, 128);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t fu[4][4];
+#pragma unroll
+      for (int kt = 0; kt < 3; ++kt) ld_frag(ex + kExU + (kt * 5 + p) * 512, fu[kt]);
+      ld_frag(ex + kExU + (kt4 * 5 + p) * 512, fu[3]);
+#pragma unroll
+      for (int b = 0; b < 5; ++b) {
+        float(&acc)[2][4] = o[b < 4 ? tri_own(b) : 2];
+        const uint32_t(&x)[4] = fu[b < 4 ? tri_kt(b) : 3];
+        mma_bf16_16816(acc[0], x, fp[b][0], fp[b][1]);
+        mma_bf16_16816(acc[1], x, fp[b][2], fp[b][3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[j] = (i == 0) == (w == 1) ? o[i][e][j] + o[2][e][j] : o[i][e][j];
+        const uint32_t y0 = movmatrix_trans(pack_bf16x2(x[0], x[1]));
+        const uint32_t y1 = movmatrix_trans(pack_bf16x2(x[2], x[3]));
+        const int t = c * kDeltaChunk + tile[i] * 16 + e * 8 + (lane >> 2);
+        if (t < at.len) {
+          uint32_t* to = reinterpret_cast<uint32_t*>(
+              a.out + ((at.first + t) * a.hv + at.h) * kDeltaDim + dv0 + (lane & 3) * 2);
+          to[0] = y0;
+          to[4] = y1;
+        }
+      }
+  }
+}
+
+__global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const DeltaArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5;
+  constexpr int kParts = kDeltaDim / kScanNV;
+  const int part = blockIdx.x % kParts;
+  const int hl = (blockIdx.x / kParts) % a.heads;
+  const int b = blockIdx.x / (kParts * a.heads);
+  ScanPlace at;
+  at.h = a.head0 + hl;
+  at.hk = at.h / (a.hv / a.hk);
+  at.first = __ldg(a.q_offsets + b);
+  at.len = (int)(__ldg(a.q_offsets + b + 1) - at.first);
+  if (at.len < a.min_len) return;
+  at.slot = delta_slot(a, b);
+  at.dvc = part * kScanNV;
+  at.items = a.ws + (delta_first_slot(a, b) * a.heads + hl) * (int64_t)kDeltaItemBytes;
+  at.item_step = (int64_t)a.heads * kDeltaItemBytes;
+  // chain warps 0 .. 2 pairs - 1, then the output warps: one of each on every scheduler
+  const int pair = (warp >> 1) % kScanPairs;
+  unsigned char* ex = smem + 2 * kScanStage + pair * kScanExch;
+  if (warp < 2 * kScanPairs) scan_chain(a, at, smem, ex, pair, warp & 1);
+  else scan_output(a, at, smem, ex, pair, warp & 1);
 }
 
 }  // namespace dsa

@@ -93,9 +93,7 @@ cudaError_t hybrid_allow_smem() {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
   cudaError_t e = allow((const void*)delta_prep_kernel, (int)sizeof(PrepSmem));
-  e = e ? e : allow((const void*)delta_scan_kernel<16>, ScanGeo<16>::kSmem);
-  e = e ? e : allow((const void*)delta_scan_kernel<32>, ScanGeo<32>::kSmem);
-  e = e ? e : allow((const void*)delta_scan_kernel<64>, ScanGeo<64>::kSmem);
+  e = e ? e : allow((const void*)delta_scan_kernel, kScanSmem);
   return e;
 }
 
@@ -358,12 +356,10 @@ dsa_status launch_recurrent(DeltaArgs a, int max_len, cudaStream_t st) {
   return launched("delta_recurrent_kernel");
 }
 
-template <int NV>
 dsa_status launch_scan(const DeltaArgs& a, cudaStream_t st) {
-  using Geo = ScanGeo<NV>;
-  const int64_t ctas = (int64_t)a.batch * a.heads * (kDeltaDim / NV);
+  const int64_t ctas = (int64_t)a.batch * a.heads * (kDeltaDim / kScanNV);
   if (ctas > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  delta_scan_kernel<NV><<<(unsigned)ctas, Geo::kThreads, Geo::kSmem, st>>>(a);
+  delta_scan_kernel<<<(unsigned)ctas, kScanThreads, kScanSmem, st>>>(a);
   return launched("delta_scan_kernel");
 }
 
@@ -420,8 +416,7 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
     a.heads = (int)std::min<int64_t>(pass, a.hv - h0);
     delta_prep_kernel<<<(unsigned)(slots * a.heads), kPrepThreads, sizeof(PrepSmem), st>>>(a);
     DSA_TRY(launched("delta_prep_kernel"));
-    if ((int64_t)a.batch * a.heads * 4 <= 2 * sms) DSA_TRY(launch_scan<32>(a, st));
-    else DSA_TRY(launch_scan<64>(a, st));
+    DSA_TRY(launch_scan(a, st));
   }
   return DSA_OK;
 }
