@@ -199,6 +199,24 @@ DSA_DEV void split_pair(float x, float y, uint32_t (&p)[N]) {
   }
 }
 
+// N pieces of the left operand made of two accumulator tiles (16 rows x 16 columns)
+template <int N>
+DSA_DEV void split_frag(const float (&x)[4], const float (&y)[4], uint32_t (&f)[N][4]) {
+  uint32_t p[N];
+  split_pair<N>(x[0], x[1], p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i][0] = p[i];
+  split_pair<N>(x[2], x[3], p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i][1] = p[i];
+  split_pair<N>(y[0], y[1], p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i][2] = p[i];
+  split_pair<N>(y[2], y[3], p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i][3] = p[i];
+}
+
 // ------------------------------------------------------------------ chunked form: T and P
 //
 // One CTA per (chunk, value head).  Each of its four warps forms 16 rows of K K^T and Q K^T up
@@ -209,21 +227,72 @@ DSA_DEV void split_pair(float x, float y, uint32_t (&p)[N]) {
 // instruction fetch.
 constexpr int kPrepThreads = 128;
 constexpr int kPrepLd = 68;  // floats per row of A: 16-byte rows, eight rows on distinct banks
-constexpr int kPrepLdM = 36;
 
 struct PrepSmem {
   union {
     struct {
       unsigned char k[kDeltaTile], q[kDeltaTile];
     };
-    struct {  // once the products are in registers
-      float A[kDeltaChunk * kPrepLd];
-      float M[32 * kPrepLdM];
-    };
+    float A[kDeltaChunk * kPrepLd];  // once the products are in registers
   };
   float2 G[kDeltaChunk];  // running sum of g, high and low part
   float ink[kDeltaChunk], inq[kDeltaChunk], beta[kDeltaChunk];
 };
+
+// Pieces of the right operand X^T (k = column of X, n = row of X) of eight rows, 16 columns.
+DSA_DEV void prep_right(const float* X, uint32_t (&f)[3][2]) {
+  const int lane = threadIdx.x & 31;
+  const float* at = X + (lane >> 2) * kPrepLd + (lane & 3) * 2;
+  uint32_t p[3];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 x = *reinterpret_cast<const float2*>(at + i * 8);
+    split_pair<3>(x.x, x.y, p);
+#pragma unroll
+    for (int m = 0; m < 3; ++m) f[m][i] = p[m];
+  }
+}
+
+// acc += the product of two operands in three pieces each
+DSA_DEV void prep_mma(float (&acc)[4], const uint32_t (&x)[3][4], const uint32_t (&y)[3][2]) {
+#pragma unroll
+  for (int px = 0; px < 3; ++px)
+#pragma unroll
+    for (int py = 0; py < 3 - px; ++py) mma_bf16_16816(acc, x[px], y[py][0], y[py][1]);
+}
+
+// Y [16 columns of T1][8 NT rows of A21] += T1^T A21^T over 16 KT rows of T1
+template <int KT, int NT>
+DSA_DEV void prep_product(const float* T1, const float* A21, float (&y)[NT][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    uint32_t fx[3][4], p[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (m, k), (m + 8, k), (m, k + 8), (m + 8, k + 8)
+      const float* at = T1 + (kt * 16 + (lane & 3) * 2 + (i >> 1) * 8) * kPrepLd + (lane >> 2) + (i & 1) * 8;
+      split_pair<3>(at[0], at[kPrepLd], p);
+#pragma unroll
+      for (int m = 0; m < 3; ++m) fx[m][i] = p[m];
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t fb[3][2];
+      prep_right(A21 + nt * 8 * kPrepLd + kt * 16, fb);
+      prep_mma(y[nt], fx, fb);
+    }
+  }
+}
+
+// T21 = -t^T: t [16 columns][8 rows]
+DSA_DEV void prep_store(float* T21, const float (&t)[4]) {
+  const int lane = threadIdx.x & 31;
+  float* at = T21 + (lane & 3) * 2 * kPrepLd + (lane >> 2);
+  at[0] = -t[0];
+  at[kPrepLd] = -t[1];
+  at[8] = -t[2];
+  at[kPrepLd + 8] = -t[3];
+}
 
 __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const DeltaArgs a) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -415,63 +484,44 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
     }
   }
   __syncthreads();
-  {  // 16 -> 32: two pairs of blocks, four values a thread
-    const int p = tid >> 6, r = (tid & 63) >> 2, c = (tid & 3) * 4;
-    float* T1 = sm.A + p * 32 * (kPrepLd + 1);
+  // The steps 16 -> 32 -> 64 on the tensor cores, transposed: Y = T1^T A21^T, then
+  // T21^T = -Y T2^T, Y going from accumulator to left operand in registers.  fp32 operands in
+  // three bf16 pieces, products below 2^-24 left out.  (As fp32 products out of shared memory
+  // these steps were half of the kernel's shared-memory traffic, which bounded it.)
+  const int part = warp & 1, half = warp >> 1;
+  {  // pair `part` of 16 x 16 blocks; rows 8 half .. of the block below
+    float* T1 = sm.A + part * 32 * (kPrepLd + 1);
     float* A21 = T1 + 16 * kPrepLd;
-    const float* T2 = A21 + 16;
-    float* M = sm.M + p * 16 * kPrepLdM;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < 16; ++k) {
-      const float x = A21[r * kPrepLd + k];
-      const float4 y = *reinterpret_cast<const float4*>(T1 + k * kPrepLd + c);
-      acc.x = fmaf(x, y.x, acc.x), acc.y = fmaf(x, y.y, acc.y);
-      acc.z = fmaf(x, y.z, acc.z), acc.w = fmaf(x, y.w, acc.w);
-    }
-    *reinterpret_cast<float4*>(M + r * kPrepLdM + c) = acc;
+    float y[2][4] = {}, t[4] = {};
+    prep_product<1, 2>(T1, A21, y);
+    uint32_t fy[3][4], fb[3][2];
+    split_frag<3>(y[0], y[1], fy);
+    prep_right(A21 + 16 + half * 8 * kPrepLd, fb);
+    prep_mma(t, fy, fb);
     __syncthreads();
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < 16; ++k) {
-      const float x = T2[r * kPrepLd + k];
-      const float4 y = *reinterpret_cast<const float4*>(M + k * kPrepLdM + c);
-      acc.x = fmaf(-x, y.x, acc.x), acc.y = fmaf(-x, y.y, acc.y);
-      acc.z = fmaf(-x, y.z, acc.z), acc.w = fmaf(-x, y.w, acc.w);
-    }
-    *reinterpret_cast<float4*>(A21 + r * kPrepLd + c) = acc;
+    prep_store(A21 + half * 8 * kPrepLd, t);
   }
   __syncthreads();
-  {  // 32 -> 64: eight values a thread
-    const int r = tid >> 2, c = (tid & 3) * 8;
+  {  // columns 16 part .. of the 32 x 32 block below, rows 16 half ..
     float* A21 = sm.A + 32 * kPrepLd;
-    const float* T2 = A21 + 32;
-    float acc[8];
-    auto product = [&](const float* x, const float* y, int ldy) {
+    float y[4][4] = {}, t[2][4] = {};
+    if (part) prep_product<1, 4>(sm.A + 16 * (kPrepLd + 1), A21 + 16, y);
+    else prep_product<2, 4>(sm.A, A21, y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll 8
-      for (int k = 0; k < 32; ++k) {
-        const float f = x[r * kPrepLd + k];
-        const float4 u = *reinterpret_cast<const float4*>(y + k * ldy + c);
-        const float4 v = *reinterpret_cast<const float4*>(y + k * ldy + c + 4);
-        acc[0] = fmaf(f, u.x, acc[0]), acc[1] = fmaf(f, u.y, acc[1]);
-        acc[2] = fmaf(f, u.z, acc[2]), acc[3] = fmaf(f, u.w, acc[3]);
-        acc[4] = fmaf(f, v.x, acc[4]), acc[5] = fmaf(f, v.y, acc[5]);
-        acc[6] = fmaf(f, v.z, acc[6]), acc[7] = fmaf(f, v.w, acc[7]);
+    for (int kt = 0; kt < 2; ++kt) {
+      if (kt > half) continue;  // T2 is lower triangular
+      uint32_t fy[3][4];
+      split_frag<3>(y[2 * kt], y[2 * kt + 1], fy);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t fb[3][2];
+        prep_right(A21 + 32 + (half * 16 + e * 8) * kPrepLd + kt * 16, fb);
+        prep_mma(t[e], fy, fb);
       }
-    };
-    product(A21, sm.A, kPrepLd);
-#pragma unroll
-    for (int i = 0; i < 8; i += 4)
-      *reinterpret_cast<float4*>(sm.M + r * kPrepLdM + c + i) =
-          make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    }
     __syncthreads();
-    product(T2, sm.M, kPrepLdM);
 #pragma unroll
-    for (int i = 0; i < 8; i += 4)
-      *reinterpret_cast<float4*>(A21 + r * kPrepLd + c + i) =
-          make_float4(-acc[i], -acc[i + 1], -acc[i + 2], -acc[i + 3]);
+    for (int e = 0; e < 2; ++e) prep_store(A21 + (half * 16 + e * 8) * kPrepLd + part * 16, t[e]);
   }
   __syncthreads();
   // T diag(beta) in three pieces, eight columns at a time
@@ -481,10 +531,11 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
     if (c >= 2 * ((i >> 4) + 1)) continue;
     uint32_t p[4][3];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 t = *reinterpret_cast<const float2*>(sm.A + i * kPrepLd + c * 8 + e * 2);
-      const float2 w = *reinterpret_cast<const float2*>(sm.beta + c * 8 + e * 2);
-      split_pair<3>(t.x * w.x, t.y * w.y, p[e]);
+    for (int e = 0; e < 2; ++e) {
+      const float4 t = *reinterpret_cast<const float4*>(sm.A + i * kPrepLd + c * 8 + e * 4);
+      const float4 w = *reinterpret_cast<const float4*>(sm.beta + c * 8 + e * 4);
+      split_pair<3>(t.x * w.x, t.y * w.y, p[2 * e]);
+      split_pair<3>(t.z * w.z, t.w * w.w, p[2 * e + 1]);
     }
 #pragma unroll
     for (int m = 0; m < 3; ++m)
@@ -566,24 +617,6 @@ DSA_DEV void ld_frag(const unsigned char* p, uint32_t (&f)[4]) {
   f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
 }
 
-// N pieces of the left operand made of two accumulator tiles (16 rows x 16 columns)
-template <int N>
-DSA_DEV void split_frag(const float (&x)[4], const float (&y)[4], uint32_t (&f)[N][4]) {
-  uint32_t p[N];
-  split_pair<N>(x[0], x[1], p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i][0] = p[i];
-  split_pair<N>(x[2], x[3], p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i][1] = p[i];
-  split_pair<N>(y[0], y[1], p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i][2] = p[i];
-  split_pair<N>(y[2], y[3], p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i][3] = p[i];
-}
-
 // The five (token tile, key token tile) blocks of a triangular product that warp w of a pair
 // computes, its tiles being 0 and 3 or 1 and 2.  Both warps run the same code (twice the code
 // was bound by instruction fetch): blocks 0 .. 3 are (second, 0), (first, 0), (second, 1),
@@ -663,7 +696,6 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
       st_frag(ex + kExS + ((w * 4 + kt) * 2) * 512, fs[kt][0]);
       st_frag(ex + kExS + ((w * 4 + kt) * 2 + 1) * 512, fs[kt][1]);
     }
-    named_barrier_arrive(bar + 1, 128);  // the output warps may read S
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
       if (kt < 3) load_k(kt + 1, fb[(kt + 1) & 1]);
@@ -676,6 +708,9 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
           mma_bf16_16816(r[2 * np + 1], fs[kt][p], f[2], f[3]);
         }
     }
+    // The output warps may read S: not before, so that their products take the tensor pipe while
+    // this warp exchanges and rounds.
+    named_barrier_arrive(bar + 1, 128);
     // the other warp's tokens to it, its share of the own tokens from it
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -744,7 +779,7 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
           mma_bf16_16816(acc[1], x, ft[b][pt][2], ft[b][pt][3]);
         }
     }
-    // U in two pieces for O, U' = U diag(t) in three for S
+    // U to the output warps, U' = U diag(t) in three pieces for S
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x[2][4], y[2][4];
@@ -762,49 +797,57 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
         y[e][2] = x[e][2] * tv.x;
         y[e][3] = x[e][3] * tv.y;
       }
-      uint32_t f2[2][4], f3[3][4];
+      uint32_t f3[3][4];
       split_frag<3>(y[0], y[1], f3);
-      split_frag<2>(x[0], x[1], f2);
       unsigned char* to = ex + kExU + tile[i] * 5 * 512;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) st_frag(to + p * 512, f2[p]);
-#pragma unroll
       for (int p = 0; p < 3; ++p) st_frag(to + (2 + p) * 512, f3[p]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float4*>(to + e * 512) = make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
     }
     // S = e^(G_C) S + U'^T K over this warp's key columns
-    auto load_kt = [&](int kt, uint32_t (&f)[4][4]) {
-#pragma unroll
-      for (int np = 0; np < 4; ++np)
-        ldmatrix_x4_trans(
-            sk + swz256(kt * 16 + (mi & 1) * 8 + mr, w * 8 + np * 2 + (mi >> 1)), f[np]);
+    // (32 at a time, so that the first half is rounded for the next chunk under the second)
+    auto load_kt = [&](int half, int kt, uint32_t (&f)[4]) {
+      ldmatrix_x4_trans(sk + swz256(kt * 16 + (mi & 1) * 8 + mr, w * 8 + half * 2 + (mi >> 1)), f);
     };
-    load_kt(0, fb[0]);
+#pragma unroll
+    for (int np = 0; np < 2; ++np) {
+      load_kt(np, 0, fb[0][np]);
+      load_kt(np, 1, fb[0][2 + np]);
+    }
     const float decay = scal[192];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[n][i] *= decay;
     named_barrier(bar + 2, 128);
-    uint32_t fu[2][3][4];
-    auto load_u = [&](int kt, uint32_t (&f)[3][4]) {
+    uint32_t fu[4][3][4];
 #pragma unroll
-      for (int p = 0; p < 3; ++p) ld_frag(ex + kExU + (kt * 5 + 2 + p) * 512, f[p]);
-    };
-    load_u(0, fu[0]);
+    for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-      if (kt < 3) {
-        load_kt(kt + 1, fb[(kt + 1) & 1]);
-        load_u(kt + 1, fu[(kt + 1) & 1]);
+      for (int p = 0; p < 3; ++p) ld_frag(ex + kExU + (kt * 5 + 2 + p) * 512, fu[kt][p]);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {  // half g >> 1 of the columns, token tiles 2 (g & 1) and the next
+      if (g < 3) {
+#pragma unroll
+        for (int np = 0; np < 2; ++np) {
+          load_kt(((g + 1) >> 1) * 2 + np, 2 * ((g + 1) & 1), fb[(g + 1) & 1][np]);
+          load_kt(((g + 1) >> 1) * 2 + np, 2 * ((g + 1) & 1) + 1, fb[(g + 1) & 1][2 + np]);
+        }
       }
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
+      for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          const uint32_t(&f)[4] = fb[kt & 1][np];
-          mma_bf16_16816(s[2 * np], fu[kt & 1][p], f[0], f[1]);
-          mma_bf16_16816(s[2 * np + 1], fu[kt & 1][p], f[2], f[3]);
-        }
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int np = 0; np < 2; ++np) {
+            const uint32_t(&f)[4] = fb[g & 1][kt * 2 + np];
+            const uint32_t(&x)[4] = fu[2 * (g & 1) + kt][p];
+            const int n = (g >> 1) * 4 + np * 2;
+            mma_bf16_16816(s[n], x, f[0], f[1]);
+            mma_bf16_16816(s[n + 1], x, f[2], f[3]);
+          }
     }
   }
   if (a.state_out && at.slot >= 0) {
@@ -904,16 +947,24 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
         o[i][e][3] *= bv.y;
       }
     named_barrier(bar + 2, 128);
+    uint32_t fu[4][2][4];  // U in two pieces
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+      float x[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 v =
+            *reinterpret_cast<const float4*>(ex + kExU + ((kt < 3 ? kt : kt4) * 5 + e) * 512);
+        x[e][0] = v.x, x[e][1] = v.y, x[e][2] = v.z, x[e][3] = v.w;
+      }
+      split_frag<2>(x[0], x[1], fu[kt]);
+    }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      uint32_t fu[4][4];
-#pragma unroll
-      for (int kt = 0; kt < 3; ++kt) ld_frag(ex + kExU + (kt * 5 + p) * 512, fu[kt]);
-      ld_frag(ex + kExU + (kt4 * 5 + p) * 512, fu[3]);
 #pragma unroll
       for (int b = 0; b < 5; ++b) {
         float(&acc)[2][4] = o[b < 4 ? tri_own(b) : 2];
-        const uint32_t(&x)[4] = fu[b < 4 ? tri_kt(b) : 3];
+        const uint32_t(&x)[4] = fu[b < 4 ? tri_kt(b) : 3][p];
         mma_bf16_16816(acc[0], x, fp[b][0], fp[b][1]);
         mma_bf16_16816(acc[1], x, fp[b][2], fp[b][3]);
       }
