@@ -203,11 +203,25 @@ dsa_status device_setup(DeviceState** out) {
 
 }  // namespace
 
-dsa_status hybrid_device(int* num_sms) {
+dsa_status hybrid_device(HybridDevice* out) {
   DeviceState* dev = nullptr;
   const dsa_status s = device_setup(&dev);
-  if (s == DSA_OK) *num_sms = dev->num_sms;
+  if (s == DSA_OK) *out = {dev->num_sms, dev->status};
   return s;
+}
+
+dsa_status make_row_map(CUtensorMap* map, const void* base, int64_t rows, int64_t width,
+                        int64_t stride, int box_cols, int box_rows) {
+  cuuint64_t gdim[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  cuuint64_t gstride[1] = {(cuuint64_t)stride * 2};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  cuuint32_t estride[2] = {1u, 1u};
+  const CUresult r = g_encode(
+      map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim, gstride, box,
+      estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_INVALID_ARG;
 }
 
 void count_launches(int n) { t_launches += n; }

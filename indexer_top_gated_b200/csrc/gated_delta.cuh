@@ -52,6 +52,13 @@ struct DeltaArgs {
   // chunked form
   unsigned char* ws;     // kDeltaItemBytes per (chunk slot, head of the pass)
   int head0, heads;      // heads of the pass
+  int* status;           // device status word
+};
+
+// The rows of q, k and v as TMA sees them: boxes of 64 rows, 64 columns of q and k (128-byte
+// swizzle) and kScanNV of v (64-byte swizzle).
+struct DeltaMaps {
+  CUtensorMap q, k, v;
 };
 
 // The state slot of sequence b, or -1: none (starts from zero, is not kept).
@@ -174,17 +181,43 @@ DSA_DEV int64_t delta_first_slot(const DeltaArgs& a, int b) {
   return (int64_t)__ldg(a.q_offsets + b) / kDeltaChunk + b;
 }
 
-// One item of the workspace, in the order in which the scan keeps it in shared memory: three
-// pieces of T, P (bf16 [64][64] each, rows of 128 bytes whose 16-byte units are permuted by
-// unit ^ (row & 7), which makes ldmatrix free of bank conflicts; the 16 x 16 blocks above the
-// diagonal are neither written nor read), then the scalars of the tokens.
-constexpr int kDeltaMat = kDeltaChunk * kDeltaChunk * 2;
+// One item of the workspace, as the scan keeps it in shared memory: three pieces of T, P (bf16),
+// each the ten 16 x 16 blocks on and below the diagonal in row order, 512 bytes a block: 16 rows
+// of two 16-byte units, which trade places in rows 4 .. 7 and 12 .. 15 (ldmatrix then meets no
+// bank conflict); then the scalars of the tokens.
+constexpr int kDeltaMat = 10 * 512;
 constexpr int kDeltaScal = 4 * kDeltaMat;        // a[64], t[64], b[64], e^(G_C)
 constexpr int kDeltaItemBytes = kDeltaScal + 1024;
-constexpr int kDeltaTile = kDeltaChunk * kDeltaDim * 2;  // K or Q of a chunk: rows of 256 bytes
+constexpr int kDeltaTile = kDeltaChunk * kDeltaDim * 2;  // K or Q of a chunk: two halves of the
+                                                         // columns, rows of 128 bytes each
+// 16-byte unit of row r, columns 8 unit .. of the triangular matrices
+DSA_DEV int tri_unit(int r, int unit) {
+  const int m = r >> 4;
+  return (((m * (m + 1)) >> 1) + (unit >> 1)) * 512 + (r & 15) * 32 +
+         (((unit & 1) ^ ((r >> 2) & 1)) << 4);
+}
 
-DSA_DEV uint32_t swz256(int row, int unit) { return row * 256 + ((unit ^ (row & 7)) << 4); }
-DSA_DEV uint32_t swz128(int row, int unit) { return row * 128 + ((unit ^ (row & 7)) << 4); }
+// 16-byte unit (columns 8 unit ..) of a row of a K or Q tile
+DSA_DEV uint32_t swz(int row, int unit) {
+  return (unit >> 3) * (kDeltaTile / 2) + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
+}
+
+// K and Q of the chunk at row0, head hk, onto `bar` (kDeltaTile bytes each); one thread.
+DSA_DEV void delta_load_qk(const DeltaMaps& maps, uint32_t k, uint32_t q, uint32_t bar, int hk,
+                           int64_t row0) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    tma_load_2d(k + i * (kDeltaTile / 2), &maps.k, bar, hk * kDeltaDim + i * 64, (int)row0);
+    tma_load_2d(q + i * (kDeltaTile / 2), &maps.q, bar, hk * kDeltaDim + i * 64, (int)row0);
+  }
+}
+
+// Zeros in rows valid .. 63 of a tile with `row_bytes` per row (TMA brought the next
+// sequence's); thread t of n.
+DSA_DEV void delta_zero_rows(unsigned char* tile, int row_bytes, int valid, int t, int n) {
+  for (int at = valid * row_bytes + t * 16; at < kDeltaChunk * row_bytes; at += n * 16)
+    *reinterpret_cast<uint4*>(tile + at) = make_uint4(0, 0, 0, 0);
+}
 
 // Two fp32 values as N packed pairs of bf16 whose sum they are, largest first.
 template <int N>
@@ -235,6 +268,8 @@ struct PrepSmem {
     };
     float A[kDeltaChunk * kPrepLd];  // once the products are in registers
   };
+  uint64_t bar;
+  int abort;
   float2 G[kDeltaChunk];  // running sum of g, high and low part
   float ink[kDeltaChunk], inq[kDeltaChunk], beta[kDeltaChunk];
 };
@@ -294,8 +329,9 @@ DSA_DEV void prep_store(float* T21, const float (&t)[4]) {
   at[kPrepLd + 8] = -t[3];
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const DeltaArgs a) {
-  extern __shared__ __align__(128) unsigned char smem_raw[];
+__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
+    const DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t item = blockIdx.x;
@@ -315,20 +351,14 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
   const int hk = h / (a.hv / a.hk);
 
   const uint32_t sk = smem_u32(sm.k), sq = smem_u32(sm.q);
-  {
-    const int r0 = tid >> 4, c = tid & 15;
-    const __nv_bfloat16* k = a.k + row0 * a.k_stride + hk * kDeltaDim + c * 8;
-    const __nv_bfloat16* q = a.q + row0 * a.q_stride + hk * kDeltaDim + c * 8;
-#pragma unroll
-    for (int i = 0; i < kDeltaTile / 16 / kPrepThreads; ++i) {
-      const int r = r0 + i * (kPrepThreads / 16);
-      const bool in = r < valid;
-      const int64_t rr = in ? r : 0;
-      cp_async_16(sk + swz256(r, c), k + rr * a.k_stride, in ? 16 : 0);
-      cp_async_16(sq + swz256(r, c), q + rr * a.q_stride, in ? 16 : 0);
-    }
+  const uint32_t bar = smem_u32(&sm.bar);
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+    mbar_arrive_expect_tx(bar, 2 * kDeltaTile);
+    delta_load_qk(maps, sk, sq, bar, hk, row0);
   }
-  cp_async_commit();
   if (warp == 0) {
     // running sum of g, two tokens a lane, in fp64 and then as a pair of fp32.  -inf (alpha = 0)
     // becomes a finite decay that is 0 all the same, so that differences of sums behind it stay
@@ -359,8 +389,13 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
       sm.beta[t] = t < valid ? __ldg(a.beta + (row0 + t) * a.hv + h) : 0.f;
     }
   }
-  cp_async_wait<0>();
-  __syncthreads();
+  __syncthreads();  // the barrier is there to wait for
+  mbar_wait_bounded(bar, 0, a.status, &sm.abort);
+  if (valid < kDeltaChunk) {
+    for (int i = 0; i < 4; ++i)
+      delta_zero_rows(sm.k + i * (kDeltaTile / 2), 128, valid, tid, kPrepThreads);
+    __syncthreads();
+  }
   {
     const int r = tid & 63;
     const unsigned char* tile = tid < 64 ? sm.k : sm.q;
@@ -368,7 +403,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
     if (a.norm) {
 #pragma unroll 4
       for (int c = 0; c < 16; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(tile + swz256(r, c));
+        const uint4 x = *reinterpret_cast<const uint4*>(tile + swz(r, c));
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -392,13 +427,13 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
 #pragma unroll 2
   for (int kt = 0; kt < 8; ++kt) {
     uint32_t fk[4], fq[4];
-    ldmatrix_x4(sk + swz256(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fk);
-    ldmatrix_x4(sq + swz256(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fq);
+    ldmatrix_x4(sk + swz(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fk);
+    ldmatrix_x4(sq + swz(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fq);
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       if (np <= mt) {
         uint32_t fb[4];
-        ldmatrix_x4(sk + swz256(np * 16 + (mi >> 1) * 8 + mr, kt * 2 + (mi & 1)), fb);
+        ldmatrix_x4(sk + swz(np * 16 + (mi >> 1) * 8 + mr, kt * 2 + (mi & 1)), fb);
         mma_bf16_16816(kk[np * 2], fk, fb[0], fb[1]);
         mma_bf16_16816(kk[np * 2 + 1], fk, fb[2], fb[3]);
         mma_bf16_16816(qk[np * 2], fq, fb[0], fb[1]);
@@ -445,7 +480,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
         x.x = j < i ? fa[half] * d0 * kk[nt][half * 2] : 0.f;
         x.y = j + 1 < i ? fa[half] * d1 * kk[nt][half * 2 + 1] : 0.f;
         *reinterpret_cast<float2*>(sm.A + i * kPrepLd + j) = x;
-        *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + swz128(i, nt) + (lane & 3) * 4) =
+        *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + tri_unit(i, nt) + (lane & 3) * 4) =
             pack_bf16x2(j <= i ? fp[half] * d0 * qk[nt][half * 2] : 0.f,
                         j < i ? fp[half] * d1 * qk[nt][half * 2 + 1] : 0.f);
       }
@@ -539,7 +574,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
     }
 #pragma unroll
     for (int m = 0; m < 3; ++m)
-      *reinterpret_cast<uint4*>(dst + m * kDeltaMat + swz128(i, c)) =
+      *reinterpret_cast<uint4*>(dst + m * kDeltaMat + tri_unit(i, c)) =
           make_uint4(p[0][m], p[1][m], p[2][m], p[3][m]);
   }
 }
@@ -554,60 +589,37 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(const Delta
 // value columns.  Two carry the chain R -> X -> U -> S: each owns 64 of the key columns of S (32
 // registers) and two of the four 16-token tiles, {0, 3} or {1, 2} (equal work in the triangular
 // products), and three exchanges through shared memory a chunk bring the halves of R together
-// and hand X and U around.  The other two, off the chain, load the next chunk and compute O.
+// and hand X and U around.  The other two, off the chain, compute O.  A ninth warp loads, by TMA
+// into two stages.
 // What bounds it: the chain's latency (220 tensor instructions a warp and chunk, which depend on
 // one another in four stages); the tensor pipe, which the output warps fill in the gaps, is the
 // next limit (304 a scheduler and chunk).  So accumulators alternate, eight or six between two
 // uses of one, and operands are fetched one step ahead.
 constexpr int kScanNV = 32;
 constexpr int kScanPairs = kScanNV / 16;
-constexpr int kScanThreads = kScanPairs * 128;
-constexpr int kScanLoaders = kScanPairs * 64;  // the output warps' threads
-// one chunk's operands: K, Q, the workspace item, V
-constexpr int kScanItem = 2 * kDeltaTile;
-constexpr int kScanV = kScanItem + kDeltaItemBytes;
-constexpr int kScanStage = kScanV + kDeltaChunk * kScanNV * 2;
+constexpr int kScanWorkers = kScanPairs * 4;  // warps
+constexpr int kScanThreads = kScanWorkers * 32 + 32;
+// one chunk's operands: K, Q, V, the workspace item
+constexpr int kScanV = 2 * kDeltaTile;
+constexpr int kScanItem = kScanV + kDeltaChunk * kScanNV * 2;
+constexpr int kScanBytes = kScanItem + kDeltaItemBytes;
+constexpr int kScanStage = (kScanBytes + 1023) / 1024 * 1024;
 // exchange areas of 16 value columns, 512 bytes (a fragment of a warp) each unit: S [8 key tiles]
 // [2 pieces], R [2 warps][4], X [4 token tiles][3 pieces], U and U' [4 token tiles][2 + 3]
 constexpr int kExS = 0, kExR = kExS + 16 * 512, kExX = kExR + 8 * 512, kExU = kExX + 12 * 512;
 constexpr int kScanExch = kExU + 20 * 512;
-constexpr int kScanSmem = 2 * kScanStage + kScanPairs * kScanExch;
+constexpr int kScanBars = 2 * kScanStage + kScanPairs * kScanExch;
+constexpr int kScanSmem = kScanBars + 64;
+
+// Barriers of the two stages: full (the loader's bytes), empty (the worker warps); of the last
+// chunk's rows; and the flag that a wait has given up.
+struct ScanSync {
+  uint64_t full[2], empty[2], tail;
+  int abort;
+};
 
 // 16-byte unit u (value columns 8u .. 8u+7) of token r in the V tile, rows of 64 bytes
 DSA_DEV uint32_t swz64(int r, int u) { return r * 64 + ((u ^ ((r >> 1) & 3)) << 4); }
-
-DSA_DEV void scan_load(const DeltaArgs& a, int tid, uint32_t stage, int64_t row0, int valid, int h,
-                       int hk, int dv0, const unsigned char* item) {
-#pragma unroll
-  for (int i = 0; i < kDeltaTile / 16 / kScanLoaders; ++i) {
-    const int at = tid + i * kScanLoaders, r = at >> 4, c = at & 15;
-    const bool in = r < valid;
-    const int64_t row = row0 + (in ? r : 0);
-    cp_async_16(stage + swz256(r, c), a.k + row * a.k_stride + hk * kDeltaDim + c * 8, in ? 16 : 0);
-    cp_async_16(stage + kDeltaTile + swz256(r, c), a.q + row * a.q_stride + hk * kDeltaDim + c * 8,
-                in ? 16 : 0);
-  }
-  // T and P: the units of the 16 x 16 blocks up to the diagonal
-#pragma unroll
-  for (int i = 0; i < 4 * kDeltaMat / 16 / kScanLoaders; ++i) {
-    const int at = tid + i * kScanLoaders, r = (at >> 3) & 63, c = (at & 7) ^ (r & 7);
-    if (c < 2 * ((r >> 4) + 1)) cp_async_16(stage + kScanItem + at * 16, item + at * 16, 16);
-  }
-  if (tid < 52)
-    cp_async_16(stage + kScanItem + kDeltaScal + tid * 16, item + kDeltaScal + tid * 16, 16);
-#pragma unroll
-  for (int i = 0; i < kDeltaChunk * kScanNV / 8 / kScanLoaders; ++i) {
-    const int at = tid + i * kScanLoaders, r = at >> 2, c = at & 3;
-    const bool in = r < valid;
-    const int64_t row = row0 + (in ? r : 0);
-    cp_async_16(stage + kScanV + swz64(r, c),
-                a.v + row * a.v_stride + (int64_t)h * kDeltaDim + dv0 + c * 8, in ? 16 : 0);
-  }
-}
-
-DSA_DEV void named_barrier_arrive(int id, int count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
 
 DSA_DEV void st_frag(unsigned char* p, const uint32_t (&f)[4]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(f[0], f[1], f[2], f[3]);
@@ -632,9 +644,41 @@ struct ScanPlace {
   int64_t item_step;
 };
 
+// The loader, one warp: chunk by chunk into the two stages as they come free.
+DSA_DEV void scan_loader(const DeltaArgs& a, const DeltaMaps& maps, const ScanPlace& at,
+                         unsigned char* smem, ScanSync* sy) {
+  const int lane = threadIdx.x & 31;
+  const int n_chunks = (at.len + kDeltaChunk - 1) / kDeltaChunk;
+  for (int c = 0; c < n_chunks; ++c) {
+    const int valid = at.len - c * kDeltaChunk;
+    if (c >= 2) mbar_wait_bounded(smem_u32(&sy->empty[c & 1]), (c >> 1) + 1 & 1, a.status, &sy->abort);
+    const bool part = valid < kDeltaChunk;
+    const uint32_t full = smem_u32(&sy->full[c & 1]);
+    const uint32_t bar = part ? smem_u32(&sy->tail) : full;
+    unsigned char* to = smem + (c & 1) * kScanStage;
+    const uint32_t stage = smem_u32(to);
+    const int64_t row0 = at.first + (int64_t)c * kDeltaChunk;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, kScanBytes);
+      delta_load_qk(maps, stage, stage + kDeltaTile, bar, at.hk, row0);
+      tma_load_2d(stage + kScanV, &maps.v, bar, at.h * kDeltaDim + at.dvc, (int)row0);
+      bulk_load(stage + kScanItem, at.items + c * at.item_step, kDeltaItemBytes, bar);
+    }
+    __syncwarp();
+    if (part) {  // the last chunk: the rows behind the sequence's end become zeros first
+      mbar_wait_bounded(bar, 0, a.status, &sy->abort);
+      for (int i = 0; i < 4; ++i)
+        delta_zero_rows(to + i * (kDeltaTile / 2), 128, valid, lane, 32);
+      delta_zero_rows(to + kScanV, kScanNV * 2, valid, lane, 32);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+    }
+  }
+}
+
 // The chain: warp w of the pair whose exchange area is ex.
 DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* smem,
-                        unsigned char* ex, int pair, int w) {
+                        ScanSync* sy, unsigned char* ex, int pair, int w) {
   const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
   const int dv0 = at.dvc + pair * 16;
   const int bar = 1 + 3 * pair;
@@ -658,19 +702,20 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
   }
 
   const uint32_t stage0 = smem_u32(smem);
-  // byte offsets of this lane's ldmatrix rows: K's token tiles (own first), T's own tiles
+  // byte offsets of this lane's ldmatrix rows: K's token tiles (own first) in this warp's half of
+  // the columns, T's blocks (0, 0) of the own tiles
   const int rb = (mi >> 1) * 8 + mr;
   uint32_t k_row[4], t_row[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    k_row[i] = (tile[i] * 16 + rb) * 256;
-    k_row[2 + i] = (their[i] * 16 + rb) * 256;
-    t_row[i] = (tile[i] * 16 + rb) * 128;
+    k_row[i] = w * (kDeltaTile / 2) + (tile[i] * 16 + rb) * 128;
+    k_row[2 + i] = w * (kDeltaTile / 2) + (their[i] * 16 + rb) * 128;
+    t_row[i] = tri_unit(tile[i] * 16 + rb, mi & 1);
   }
   const int n_chunks = (at.len + kDeltaChunk - 1) / kDeltaChunk;
 #pragma unroll 1
   for (int c = 0; c < n_chunks; ++c) {
-    __syncthreads();  // chunk c is in place, and every warp is done with chunk c - 1
+    mbar_wait_bounded(smem_u32(&sy->full[c & 1]), c >> 1 & 1, a.status, &sy->abort);
     const uint32_t sk = stage0 + (c & 1) * kScanStage;
     const uint32_t st = sk + kScanItem, sv = sk + kScanV;
     const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * kScanStage + kScanItem +
@@ -684,7 +729,7 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
       for (int i = 0; i < 4; ++i) r[n][i] = 0.f;
     uint32_t fb[2][4][4];
     auto load_k = [&](int kt, uint32_t (&f)[4][4]) {
-      const uint32_t unit = ((w * 8 + kt * 2 + (mi & 1)) ^ mr) << 4;
+      const uint32_t unit = ((kt * 2 + (mi & 1)) ^ mr) << 4;
 #pragma unroll
       for (int np = 0; np < 4; ++np) ldmatrix_x4(sk + k_row[np] + unit, f[np]);
     };
@@ -708,9 +753,6 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
           mma_bf16_16816(r[2 * np + 1], fs[kt][p], f[2], f[3]);
         }
     }
-    // The output warps may read S: not before, so that their products take the tensor pipe while
-    // this warp exchanges and rounds.
-    named_barrier_arrive(bar + 1, 128);
     // the other warp's tokens to it, its share of the own tokens from it
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -725,7 +767,10 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
       for (int e = 0; e < 2; ++e)
         av[i][e] = *reinterpret_cast<const float2*>(scal + tile[i] * 16 + e * 8 + (lane & 3) * 2);
     }
-    named_barrier(bar, 64);
+    // The pair's four warps: the halves of R may be read, and S by the output warps: not before,
+    // so that their products take the tensor pipe while these exchange and round.  And the output
+    // warps are done with the last chunk's U.
+    named_barrier(bar + 1, 128);
     // X^T = V^T - R^T diag(a) of the own tokens, handed to both warps in three pieces
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -747,10 +792,10 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
     }
 #pragma unroll
     for (int b = 0; b < 5; ++b) {
-      const uint32_t row = b < 4 ? t_row[tri_own(b)] : w ? t_row[0] : t_row[1];
-      const uint32_t unit = (((b < 4 ? tri_kt(b) : kt4) * 2 + (mi & 1)) ^ mr) << 4;
+      const uint32_t row = b < 4 ? t_row[tri_own(b)] + tri_kt(b) * 512
+                                 : (w ? t_row[0] : t_row[1]) + kt4 * 512;
 #pragma unroll
-      for (int p = 0; p < 3; ++p) ldmatrix_x4(st + p * kDeltaMat + row + unit, ft[b][p]);
+      for (int p = 0; p < 3; ++p) ldmatrix_x4(st + p * kDeltaMat + row, ft[b][p]);
     }
     named_barrier(bar, 64);
 
@@ -809,7 +854,7 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
     // S = e^(G_C) S + U'^T K over this warp's key columns
     // (32 at a time, so that the first half is rounded for the next chunk under the second)
     auto load_kt = [&](int half, int kt, uint32_t (&f)[4]) {
-      ldmatrix_x4_trans(sk + swz256(kt * 16 + (mi & 1) * 8 + mr, w * 8 + half * 2 + (mi >> 1)), f);
+      ldmatrix_x4_trans(sk + swz(kt * 16 + (mi & 1) * 8 + mr, w * 8 + half * 2 + (mi >> 1)), f);
     };
 #pragma unroll
     for (int np = 0; np < 2; ++np) {
@@ -849,6 +894,8 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
             mma_bf16_16816(s[n + 1], x, f[2], f[3]);
           }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sy->empty[c & 1]));
   }
   if (a.state_out && at.slot >= 0) {
 #pragma unroll
@@ -860,11 +907,10 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
   }
 }
 
-// The output warps: the next chunk's loads, then O^T = QS^T diag(b) + U^T P^T of the own tokens.
+// The output warps: O^T = QS^T diag(b) + U^T P^T of the own tokens.
 DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char* smem,
-                         unsigned char* ex, int pair, int w) {
+                         ScanSync* sy, unsigned char* ex, int pair, int w) {
   const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
-  const int loader = (pair * 2 + w) * 32 + lane;
   const int dv0 = at.dvc + pair * 16;
   const int bar = 1 + 3 * pair;
   const int tile[2] = {tri_tile(w, 0), tri_tile(w, 1)};
@@ -874,24 +920,11 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
   const int rb = (mi >> 1) * 8 + mr;
   const int n_chunks = (at.len + kDeltaChunk - 1) / kDeltaChunk;
 
-  auto load = [&](int c) {
-    const int left = at.len - c * kDeltaChunk;
-    scan_load(a, loader, stage0 + (c & 1) * kScanStage, at.first + (int64_t)c * kDeltaChunk,
-              left < kDeltaChunk ? left : kDeltaChunk, at.h, at.hk, at.dvc,
-              at.items + c * at.item_step);
-    cp_async_commit();
-  };
-  // one copy of the loads' code: chunk c + 1 is asked for once chunk c has come
 #pragma unroll 1
-  for (int c = -1; c < n_chunks; ++c) {
-    if (c >= 0) {
-      cp_async_wait<0>();
-      __syncthreads();
-    }
-    if (c + 1 < n_chunks) load(c + 1);
-    if (c < 0) continue;
+  for (int c = 0; c < n_chunks; ++c) {
+    mbar_wait_bounded(smem_u32(&sy->full[c & 1]), c >> 1 & 1, a.status, &sy->abort);
     const uint32_t sq = stage0 + (c & 1) * kScanStage + kDeltaTile;
-    const uint32_t sp = sq + kDeltaTile + 3 * kDeltaMat;
+    const uint32_t sp = sq - kDeltaTile + kScanItem + 3 * kDeltaMat;
     const float* scal = reinterpret_cast<const float*>(smem + (c & 1) * kScanStage + kScanItem +
                                                        kDeltaScal);
     float o[3][2][4];  // first tile, second tile, block 4
@@ -905,7 +938,7 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
     auto load_q = [&](int kt, uint32_t (&f)[2][4]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        ldmatrix_x4(sq + swz256(tile[i] * 16 + rb, kt * 2 + (mi & 1)), f[i]);
+        ldmatrix_x4(sq + swz(tile[i] * 16 + rb, kt * 2 + (mi & 1)), f[i]);
     };
     auto load_s = [&](int kt, uint32_t (&f)[2][4]) {
 #pragma unroll
@@ -933,7 +966,7 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
 #pragma unroll
     for (int b = 0; b < 5; ++b) {
       const int row = (b < 4 ? tile[tri_own(b)] : kt4) * 16 + rb;
-      ldmatrix_x4(sp + swz128(row, (b < 4 ? tri_kt(b) : kt4) * 2 + (mi & 1)), fp[b]);
+      ldmatrix_x4(sp + tri_unit(row, (b < 4 ? tri_kt(b) : kt4) * 2 + (mi & 1)), fp[b]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -946,6 +979,8 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
         o[i][e][2] *= bv.x;
         o[i][e][3] *= bv.y;
       }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sy->empty[c & 1]));  // all of the chunk's has been read
     named_barrier(bar + 2, 128);
     uint32_t fu[4][2][4];  // U in two pieces
 #pragma unroll
@@ -990,8 +1025,9 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
   }
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const DeltaArgs a) {
-  extern __shared__ __align__(128) unsigned char smem[];
+__global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(
+    const DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
+  extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5;
   constexpr int kParts = kDeltaDim / kScanNV;
   const int part = blockIdx.x % kParts;
@@ -1007,11 +1043,23 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
   at.dvc = part * kScanNV;
   at.items = a.ws + (delta_first_slot(a, b) * a.heads + hl) * (int64_t)kDeltaItemBytes;
   at.item_step = (int64_t)a.heads * kDeltaItemBytes;
-  // chain warps 0 .. 2 pairs - 1, then the output warps: one of each on every scheduler
+  ScanSync* sy = reinterpret_cast<ScanSync*>(smem + kScanBars);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sy->full[i]), 1);
+      mbar_init(smem_u32(&sy->empty[i]), kScanWorkers);
+    }
+    mbar_init(smem_u32(&sy->tail), 1);
+    sy->abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  // chain warps, then output warps (one of each on every scheduler), then the loader
   const int pair = (warp >> 1) % kScanPairs;
   unsigned char* ex = smem + 2 * kScanStage + pair * kScanExch;
-  if (warp < 2 * kScanPairs) scan_chain(a, at, smem, ex, pair, warp & 1);
-  else scan_output(a, at, smem, ex, pair, warp & 1);
+  if (warp == kScanWorkers) scan_loader(a, maps, at, smem, sy);
+  else if (warp < 2 * kScanPairs) scan_chain(a, at, smem, sy, ex, pair, warp & 1);
+  else scan_output(a, at, smem, sy, ex, pair, warp & 1);
 }
 
 }  // namespace dsa

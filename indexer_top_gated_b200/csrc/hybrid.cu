@@ -201,11 +201,11 @@ dsa_status dsa_rope_append(const dsa_params* P, const dsa_ragged* R, const dsa_r
   a.idx_scale_q = P->idx_scale_q;
   a.idx_scale_k = P->idx_scale_k;
   if (R->total_q == 0 || !(att || idx)) return DSA_OK;
-  int sms = 0;
-  DSA_TRY(hybrid_device(&sms));
+  HybridDevice dev;
+  DSA_TRY(hybrid_device(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // one row per CTA until there are CTAs enough to fill the GPU several times over
-  if (R->total_q < (int64_t)sms * 32)
+  if (R->total_q < (int64_t)dev.num_sms * 32)
     rope_append_kernel<1><<<(unsigned)R->total_q, kRopeThreads, 0, st>>>(a);
   else
     rope_append_kernel<4><<<(unsigned)((R->total_q + 3) / 4), kRopeThreads, 0, st>>>(a);
@@ -270,12 +270,12 @@ dsa_status dsa_short_conv(const dsa_conv_params* P, const dsa_ragged* R, const v
   a.channels = P->channels;
   a.silu = P->silu;
   a.out = static_cast<__nv_bfloat16*>(out);
-  int sms = 0;
-  DSA_TRY(hybrid_device(&sms));
+  HybridDevice dev;
+  DSA_TRY(hybrid_device(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return P->width == 2 ? launch_conv<2>(a, R, sms, st)
-         : P->width == 3 ? launch_conv<3>(a, R, sms, st)
-                         : launch_conv<4>(a, R, sms, st);
+  return P->width == 2 ? launch_conv<2>(a, R, dev.num_sms, st)
+         : P->width == 3 ? launch_conv<3>(a, R, dev.num_sms, st)
+                         : launch_conv<4>(a, R, dev.num_sms, st);
 }
 
 }  // extern "C"
@@ -356,10 +356,10 @@ dsa_status launch_recurrent(DeltaArgs a, int max_len, cudaStream_t st) {
   return launched("delta_recurrent_kernel");
 }
 
-dsa_status launch_scan(const DeltaArgs& a, cudaStream_t st) {
+dsa_status launch_scan(const DeltaArgs& a, const DeltaMaps& maps, cudaStream_t st) {
   const int64_t ctas = (int64_t)a.batch * a.heads * (kDeltaDim / kScanNV);
   if (ctas > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  delta_scan_kernel<<<(unsigned)ctas, kScanThreads, kScanSmem, st>>>(a);
+  delta_scan_kernel<<<(unsigned)ctas, kScanThreads, kScanSmem, st>>>(a, maps);
   return launched("delta_scan_kernel");
 }
 
@@ -387,9 +387,9 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   DeltaArgs a = {};
   DSA_TRY(delta_args(P, R, q, k, v, g, beta, state_in, state_out, state_index, out, &a));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int sms = 0;
-  if (R->max_q_len <= kDeltaShort) {
-    DSA_TRY(hybrid_device(&sms));
+  HybridDevice dev;
+  if (R->max_q_len <= kDeltaShort || R->total_q == 0) {
+    DSA_TRY(hybrid_device(&dev));
     return launch_recurrent(a, INT32_MAX, st);
   }
   const int64_t slots = delta_slots(R);
@@ -400,7 +400,13 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   pass = std::min<int64_t>(pass, a.hv);
   if (slots * pass > INT32_MAX) pass = INT32_MAX / slots;
   if (pass < 1) return DSA_ERR_UNSUPPORTED;
-  DSA_TRY(hybrid_device(&sms));
+  DSA_TRY(hybrid_device(&dev));
+  a.status = dev.status;
+  DeltaMaps maps;
+  DSA_TRY(make_row_map(&maps.q, q, R->total_q, P->n_k_heads * kDeltaDim, a.q_stride, 64, kDeltaChunk));
+  DSA_TRY(make_row_map(&maps.k, k, R->total_q, P->n_k_heads * kDeltaDim, a.k_stride, 64, kDeltaChunk));
+  DSA_TRY(make_row_map(&maps.v, v, R->total_q, P->n_v_heads * kDeltaDim, a.v_stride, kScanNV,
+                       kDeltaChunk));
   bool any_short = true;
   if (R->q_offsets_host) {
     any_short = false;
@@ -414,9 +420,9 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   for (int h0 = 0; h0 < a.hv; h0 += (int)pass) {
     a.head0 = h0;
     a.heads = (int)std::min<int64_t>(pass, a.hv - h0);
-    delta_prep_kernel<<<(unsigned)(slots * a.heads), kPrepThreads, sizeof(PrepSmem), st>>>(a);
+    delta_prep_kernel<<<(unsigned)(slots * a.heads), kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
     DSA_TRY(launched("delta_prep_kernel"));
-    DSA_TRY(launch_scan(a, st));
+    DSA_TRY(launch_scan(a, maps, st));
   }
   return DSA_OK;
 }
@@ -429,8 +435,8 @@ dsa_status dsa_gated_delta_decode(const dsa_delta_params* P, const dsa_ragged* R
   if (R->max_q_len > 1 || R->total_q > R->batch) return DSA_ERR_INVALID_ARG;
   DeltaArgs a = {};
   DSA_TRY(delta_args(P, R, q, k, v, g, beta, state_in, state_out, state_index, out, &a));
-  int sms = 0;
-  DSA_TRY(hybrid_device(&sms));
+  HybridDevice dev;
+  DSA_TRY(hybrid_device(&dev));
   return launch_recurrent(a, INT32_MAX, static_cast<cudaStream_t>(stream));
 }
 

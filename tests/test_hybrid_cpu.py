@@ -165,8 +165,9 @@ def test_delta_decode_is_one_token_per_sequence(dsa):
 def test_delta_workspace(dsa):
     shape = dsa.DeltaShape(2, 4)
     mn, rec = dsa.dsa_gated_delta_workspace_size(shape, _rg(dsa, batch=3, q=1000))
-    # per chunk and head: three pieces of the inverse and P, 64 x 64 bf16 each, and the scalars
-    assert mn == (3000 // 64 + 3) * (4 * 64 * 64 * 2 + 1024) and rec == 4 * mn
+    # per chunk and head: three pieces of the inverse and P, ten 16 x 16 bf16 blocks each, and the
+    # scalars
+    assert mn == (3000 // 64 + 3) * (4 * 10 * 512 + 1024) and rec == 4 * mn
     assert dsa.dsa_gated_delta_workspace_size(shape, _rg(dsa, batch=3, q=16)) == (0, 0)
     W = dsa.DSA_ERR_WORKSPACE
     assert _delta(dsa, ws=None) == W
