@@ -368,7 +368,7 @@ def dsa_decode_noalloc(shape: LayerShape, rg: Ragged, q_idx, k_idx, w, q, k_cach
 # row strides come from the tensors, and types, sizes and the device are checked here, since the
 # library sees addresses only.
 
-@dataclass
+@dataclass(frozen=True)
 class RopeShape:
     """Rotary layout, the rotated part of a head, and its frequencies (dsa_rope_params)."""
     layout: int = DSA_ROPE_HALF
@@ -384,8 +384,17 @@ class RopeShape:
     beta_slow: float = 1.0
     magnitude: float = 1.0
 
+    def __post_init__(self):
+        object.__setattr__(self, "_params", RopeParams(
+            self.layout, self.scaling, self.rot_dim, self.rot_offset, self.idx_rot_dim,
+            self.idx_rot_offset, self.theta, self.factor, self.orig_len, self.beta_fast,
+            self.beta_slow, self.magnitude))
 
-@dataclass
+    def params(self) -> RopeParams:
+        return RopeParams.from_buffer_copy(self._params)
+
+
+@dataclass(frozen=True)
 class ConvShape:
     """Channels, taps and activation of the short convolution (dsa_conv_params)."""
     channels: int
@@ -393,7 +402,7 @@ class ConvShape:
     silu: bool = True
 
 
-@dataclass
+@dataclass(frozen=True)
 class DeltaShape:
     """Heads and numerics of the gated delta rule (dsa_delta_params)."""
     n_k_heads: int
@@ -412,7 +421,8 @@ def _tensor(where, name, t, dtype, shape, device) -> int:
     """Address of a dense tensor of at least shape[0] rows and exactly the other sizes."""
     if t.dtype is not dtype or t.get_device() != device:
         _bad(where, f"{name} is {t.dtype} on {t.device}, not {dtype} on cuda:{device}")
-    if t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != shape[1:]:
+    if t.shape != shape and (t.dim() != len(shape) or t.shape[0] < shape[0]
+                             or t.shape[1:] != shape[1:]):
         _bad(where, f"{name} has shape {tuple(t.shape)}, not {shape}")
     if not t.is_contiguous():
         _bad(where, f"{name} is not contiguous")
@@ -420,27 +430,36 @@ def _tensor(where, name, t, dtype, shape, device) -> int:
 
 
 def _rows(where, name, t, dtype, shape, device):
-    """Address and row stride of a tensor whose rows are dense."""
+    """Address and row stride (0: packed) of a tensor whose rows are dense."""
+    if t.is_contiguous():
+        return _tensor(where, name, t, dtype, shape, device), 0
     if t.dtype is not dtype or t.get_device() != device:
         _bad(where, f"{name} is {t.dtype} on {t.device}, not {dtype} on cuda:{device}")
-    if t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != shape[1:]:
+    if t.shape != shape and (t.dim() != len(shape) or t.shape[0] < shape[0]
+                             or t.shape[1:] != shape[1:]):
         _bad(where, f"{name} has shape {tuple(t.shape)}, not {shape}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    dense = 1
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and step != dense:
-            _bad(where, f"{name} has rows that are not dense (strides {t.stride()})")
-        dense *= size
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+    steps, dense = t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if steps[i] != dense and shape[i] > 1:
+            _bad(where, f"{name} has rows that are not dense (strides {steps})")
+        dense *= shape[i]
+    return t.data_ptr(), steps[0]
 
 
 def _device(stream) -> int:
-    import torch
-    device = torch.cuda.current_device()
+    device = _cuda().current_device()
     if stream is not None and stream.device.index != device:
-        raise DsaError(DSA_ERR_INVALID_ARG, f"stream of {stream.device} while cuda:{device} is current")
+        _bad("stream", f"of {stream.device} while cuda:{device} is current")
     return device
+
+
+def _cuda():
+    import torch
+    return torch.cuda
+
+
+def _raw_stream(stream, device) -> int:
+    return _cuda().current_stream(device).cuda_stream if stream is None else stream.cuda_stream
 
 
 def _index(where, name, t, n, device):
@@ -457,32 +476,33 @@ def dsa_rope_append(shape: LayerShape, rg: Ragged, rope: RopeShape, q=None, k=No
     where, device = "dsa_rope_append", _device(stream)
     bf16 = torch.bfloat16
     idx_type = torch.float8_e4m3fn if shape.idx_dtype == DSA_FP8_E4M3 else bf16
-    d, di = shape.head_dim, shape.idx_dim
-    nq, nkv, ni = shape.n_q_heads, shape.n_kv_heads, shape.n_idx_heads
-    src, strides, dst = [], [], []
-    for name, t, to_name, to, heads, dim, rows, kind in (
-            ("q", q, "q_out", q_out, nq, d, rg.total_q, bf16),
-            ("k", k, "k_cache", k_cache, nkv, d, rg.total_kv, bf16),
-            ("v", v, "v_cache", v_cache, nkv, d, rg.total_kv, bf16),
-            ("q_idx", q_idx, "q_idx_out", q_idx_out, ni, di, rg.total_q, idx_type),
-            ("k_idx", k_idx, "k_idx_cache", k_idx_cache, ni, di, rg.total_kv, idx_type)):
-        if t is None:
-            src.append(None), strides.append(0), dst.append(None)
-            continue
+    o, b = rope.params(), RopeBuffers()
+    n, rows, d, di = rg.total_q, rg.total_kv, shape.head_dim, shape.idx_dim
+
+    def put(name, t, to_name, to, heads, dim, to_rows, to_type):
         if to is None:
             _bad(where, f"{name} without {to_name}")
-        p, step = _rows(where, name, t, bf16, (rg.total_q, heads, dim), device)
-        src.append(p), strides.append(step)
-        dst.append(_tensor(where, to_name, to, kind, (rows, heads, dim), device))
-    o = RopeParams(rope.layout, rope.scaling, rope.rot_dim, rope.rot_offset, rope.idx_rot_dim,
-                   rope.idx_rot_offset, rope.theta, rope.factor, rope.orig_len, rope.beta_fast,
-                   rope.beta_slow, rope.magnitude, *strides)
-    b = RopeBuffers(*src, dst[0], dst[1], dst[2], dst[3], dst[4])
-    p = shape.params()
-    _check(lib.dsa_rope_append(ctypes.byref(p), ctypes.byref(rg), ctypes.byref(o), ctypes.byref(b),
-                               _index(where, "positions", positions, rg.total_q, device),
-                               _index(where, "err_count", err_count, 1, device),
-                               _stream(stream)), where)
+        at, step = _rows(where, name, t, bf16, (n, heads, dim), device)
+        setattr(b, name, at)
+        if step:
+            setattr(o, name + "_row_stride", step)
+        setattr(b, to_name, _tensor(where, to_name, to, to_type, (to_rows, heads, dim), device))
+
+    if q is not None:
+        put("q", q, "q_out", q_out, shape.n_q_heads, d, n, bf16)
+    if k is not None:
+        put("k", k, "k_cache", k_cache, shape.n_kv_heads, d, rows, bf16)
+    if v is not None:
+        put("v", v, "v_cache", v_cache, shape.n_kv_heads, d, rows, bf16)
+    if q_idx is not None:
+        put("q_idx", q_idx, "q_idx_out", q_idx_out, shape.n_idx_heads, di, n, idx_type)
+    if k_idx is not None:
+        put("k_idx", k_idx, "k_idx_cache", k_idx_cache, shape.n_idx_heads, di, rows, idx_type)
+    rc = lib.dsa_rope_append(ctypes.byref(shape.params()), ctypes.byref(rg), ctypes.byref(o),
+                             ctypes.byref(b), _index(where, "positions", positions, n, device),
+                             _index(where, "err_count", err_count, 1, device),
+                             _raw_stream(stream, device))
+    _check(rc, where)
 
 
 def dsa_short_conv(conv: ConvShape, rg: Ragged, x, weight, out, bias=None, state_in=None,
@@ -496,15 +516,20 @@ def dsa_short_conv(conv: ConvShape, rg: Ragged, x, weight, out, bias=None, state
     po, so = _rows(where, "out", out, bf16, (rg.total_q, c), device)
     pw = _tensor(where, "weight", weight, bf16, (c, conv.width), device)
     pb = None if bias is None else _tensor(where, "bias", bias, bf16, (c,), device)
-    slots = [t.shape[0] for t in (state_in, state_out) if t is not None]
-    n = min(slots) if slots else 0
-    s0, s1 = (None if t is None else
-              _tensor(where, name, t, bf16, (n, conv.width - 1, c), device)
-              for name, t in (("state_in", state_in), ("state_out", state_out)))
+    n, s0, s1 = _states(where, state_in, state_out, bf16, (conv.width - 1, c), device)
     p = ConvParams(c, conv.width, int(conv.silu), n, sx, so)
     _check(lib.dsa_short_conv(ctypes.byref(p), ctypes.byref(rg), px, pw, pb, s0, s1,
                               _index(where, "state_index", state_index, rg.batch, device), po,
-                              _stream(stream)), where)
+                              _raw_stream(stream, device)), where)
+
+
+def _states(where, state_in, state_out, dtype, slot, device):
+    """Slots and addresses of the states before and after (either may be None)."""
+    n = 0 if state_in is None and state_out is None else \
+        min(t.shape[0] for t in (state_in, state_out) if t is not None)
+    shape = (n, *slot)
+    return n, None if state_in is None else _tensor(where, "state_in", state_in, dtype, shape, device), \
+        None if state_out is None else _tensor(where, "state_out", state_out, dtype, shape, device)
 
 
 def _delta_params(delta: DeltaShape, n_states: int = 0, strides=(0, 0, 0)) -> DeltaParams:
@@ -515,17 +540,15 @@ def _delta_params(delta: DeltaShape, n_states: int = 0, strides=(0, 0, 0)) -> De
 def _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out, state_index, device):
     import torch
     bf16, f32 = torch.bfloat16, torch.float32
-    n, hk, hv, d = rg.total_q, delta.n_k_heads, delta.n_v_heads, delta.head_dim
-    pq, sq = _rows(where, "q", q, bf16, (n, hk, d), device)
-    pk, sk = _rows(where, "k", k, bf16, (n, hk, d), device)
-    pv, sv = _rows(where, "v", v, bf16, (n, hv, d), device)
-    pg = _tensor(where, "g", g, f32, (n, hv), device)
-    pb = _tensor(where, "beta", beta, f32, (n, hv), device)
-    po = _tensor(where, "out", out, bf16, (n, hv, d), device)
-    slots = [t.shape[0] for t in (state_in, state_out) if t is not None]
-    ns = min(slots) if slots else 0
-    s0, s1 = (None if t is None else _tensor(where, name, t, f32, (ns, hv, d, d), device)
-              for name, t in (("state_in", state_in), ("state_out", state_out)))
+    n, hv, d = rg.total_q, delta.n_v_heads, delta.head_dim
+    qk, vo, gb = (n, delta.n_k_heads, d), (n, hv, d), (n, hv)
+    pq, sq = _rows(where, "q", q, bf16, qk, device)
+    pk, sk = _rows(where, "k", k, bf16, qk, device)
+    pv, sv = _rows(where, "v", v, bf16, vo, device)
+    pg = _tensor(where, "g", g, f32, gb, device)
+    pb = _tensor(where, "beta", beta, f32, gb, device)
+    po = _tensor(where, "out", out, bf16, vo, device)
+    ns, s0, s1 = _states(where, state_in, state_out, f32, (hv, d, d), device)
     pi = _index(where, "state_index", state_index, rg.batch, device)
     return _delta_params(delta, ns, (sq, sk, sv)), (pq, pk, pv, pg, pb, s0, s1, pi, po)
 
@@ -550,7 +573,7 @@ def dsa_gated_delta_prefill(delta: DeltaShape, rg: Ragged, q, k, v, g, beta, out
     if workspace is not None and workspace.get_device() != device:
         _bad(where, f"workspace on {workspace.device}, not cuda:{device}")
     _check(lib.dsa_gated_delta_prefill(ctypes.byref(p), ctypes.byref(rg), *args, _ptr(workspace),
-                                       ws_bytes, _stream(stream)), where)
+                                       ws_bytes, _raw_stream(stream, device)), where)
 
 
 def dsa_gated_delta_decode(delta: DeltaShape, rg: Ragged, q, k, v, g, beta, out, state_in=None,
@@ -559,8 +582,8 @@ def dsa_gated_delta_decode(delta: DeltaShape, rg: Ragged, q, k, v, g, beta, out,
     where, device = "dsa_gated_delta_decode", _device(stream)
     p, args = _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out,
                           state_index, device)
-    _check(lib.dsa_gated_delta_decode(ctypes.byref(p), ctypes.byref(rg), *args, _stream(stream)),
-           where)
+    _check(lib.dsa_gated_delta_decode(ctypes.byref(p), ctypes.byref(rg), *args,
+                                      _raw_stream(stream, device)), where)
 
 
 def dsa_device_status(clear: bool = True, stream=None) -> int:

@@ -337,13 +337,9 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
   const int64_t item = blockIdx.x;
   const int64_t slot = item / a.heads;
   const int h = a.head0 + (int)(item % a.heads);
-  // the sequence whose slots hold this one
-  int lo = 0, hi = a.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (delta_first_slot(a, mid) <= slot) lo = mid;
-    else hi = mid - 1;
-  }
+  int lo = 0;  // the sequence whose slots hold this one
+  for (int i = 1; i < a.batch; i += kPrepThreads)
+    lo += __syncthreads_count(i + tid < a.batch && delta_first_slot(a, i + tid) <= slot);
   const int64_t first = __ldg(a.q_offsets + lo), end = __ldg(a.q_offsets + lo + 1);
   const int64_t row0 = first + (slot - delta_first_slot(a, lo)) * kDeltaChunk;
   if (end - first < a.min_len || row0 >= end) return;

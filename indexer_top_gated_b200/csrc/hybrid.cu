@@ -61,12 +61,16 @@ int64_t row_stride(int64_t stride, int64_t width) {
 
 // ---------------------------------------------------------------- rotary append
 dsa_status rope_freqs(const dsa_rope_params* O, int rot, double* f) {
-  double theta = O->theta;
+  if (rot == 0) return DSA_OK;
+  long double theta = O->theta;
   if (O->scaling == DSA_ROPE_SCALE_NTK && rot > 2)
-    theta *= std::pow(O->factor, (double)rot / (rot - 2));
+    theta *= std::pow((long double)O->factor, (long double)rot / (rot - 2));
   const double two_pi = 6.283185307179586477;
-  for (int i = 0; i < rot / 2; ++i) {
-    double x = std::pow(theta, -2.0 * i / rot);
+  // powers by multiplication: 64 steps in 64-bit mantissas stay below a double's half step
+  const long double ratio = std::pow(theta, -2.0L / rot);
+  long double power = 1;
+  for (int i = 0; i < rot / 2; ++i, power *= ratio) {
+    double x = (double)power;
     if (O->scaling == DSA_ROPE_SCALE_LINEAR) x /= O->factor;
     if (O->scaling == DSA_ROPE_SCALE_BY_PARTS) {
       const double turns = O->orig_len * x / two_pi;

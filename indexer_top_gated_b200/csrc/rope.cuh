@@ -130,6 +130,7 @@ DSA_DEV void rope_tensor(const RopeArgs& a, const RopeTensor& x, int64_t r0, int
   const int rot = !kRotate ? 0 : kIdx ? a.idx_rot : a.rot;
   const int off = kIdx ? a.idx_off : a.off;
   const bool inter = a.interleaved != 0;
+#pragma unroll 2
   for (int at = threadIdx.x; at < n * per_row; at += kRopeThreads) {
     const int i = at / per_row, rem = at - i * per_row;
     const int h = rem / (D / 16);
@@ -171,14 +172,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const int tid = threadIdx.x;
   const int64_t r0 = (int64_t)blockIdx.x * ROWS;
   const int n = (int)(a.total_q - r0 < ROWS ? a.total_q - r0 : ROWS);
+  const int b0 = seq_of_row_cta<kRopeThreads>(a.q_offsets, a.batch, r0);
   if (tid < n) {
     const int64_t r = r0 + tid;
     int64_t q_row = -1, c_row = -1;
     int p = 0;
     if (r < __ldg(a.q_offsets + a.batch)) {  // rows behind the last sequence stay as they are
-      const int b = seq_of_row(a.q_offsets, a.batch, r);
+      int b = b0;
+      int64_t end = __ldg(a.q_offsets + b + 1);
+      while (end <= r) end = __ldg(a.q_offsets + ++b + 1);
       const int64_t kv0 = __ldg(a.kv_offsets + b), len = __ldg(a.kv_offsets + b + 1) - kv0;
-      const int64_t at = len - (__ldg(a.q_offsets + b + 1) - r);
+      const int64_t at = len - (end - r);
       q_row = r;
       p = a.positions ? __ldg(a.positions + r) : (int)at;
       if (at >= 0) {

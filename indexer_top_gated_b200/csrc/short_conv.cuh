@@ -26,13 +26,22 @@ struct ConvArgs {
   __nv_bfloat16* out;
 };
 
-DSA_DEV void conv_unpack(uint4 x, float (&f)[8]) {
+// Two fp32 values, for the packed multiply-add of sm_100.
+DSA_DEV uint64_t f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+DSA_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+DSA_DEV void conv_unpack(uint4 x, uint64_t (&f)[4]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    f[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
 // Grid: x = channel groups, y = runs.  Run k of sequence b is run q_offsets[b] / RUN + b + k
@@ -41,24 +50,23 @@ DSA_DEV void conv_unpack(uint4 x, float (&f)[8]) {
 template <int W, int RUN>
 __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs a) {
   const int c0 = (blockIdx.x * kConvThreads + threadIdx.x) * 8;
-  if (c0 >= a.channels) return;
   const int64_t run = (int64_t)blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
-  int lo = 0, hi = a.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)__ldg(a.q_offsets + mid) / RUN + mid <= run) lo = mid;
-    else hi = mid - 1;
+  int b = 0;
+  for (int i = 1; i < a.batch; i += kConvThreads) {
+    const int at = i + threadIdx.x;
+    b += __syncthreads_count(at < a.batch && __ldg(a.q_offsets + at) / RUN + at <= run);
   }
-  const int64_t first = __ldg(a.q_offsets + lo);
-  const int64_t n = __ldg(a.q_offsets + lo + 1) - first;
-  const int64_t k = run - (first / RUN + lo);
+  if (c0 >= a.channels) return;
+  const int64_t first = __ldg(a.q_offsets + b);
+  const int64_t n = __ldg(a.q_offsets + b + 1) - first;
+  const int64_t k = run - (first / RUN + b);
   if (k > 0 && k * RUN >= n) return;
   constexpr int H = W - 1;
   const __nv_bfloat16* x = a.x + first * a.x_stride + c0;
 
   uint4 hist[H];  // the H rows before the run, oldest first
   if (k == 0) {
-    const int s = a.state_index ? __ldg(a.state_index + lo) : lo;
+    const int s = a.state_index ? __ldg(a.state_index + b) : b;
     const bool kept = s >= 0 && s < a.n_states;
     const int64_t at = (int64_t)(kept ? s : 0) * H * a.channels + c0;
 #pragma unroll
@@ -89,32 +97,27 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
       hist[j] = __ldg(reinterpret_cast<const uint4*>(x + (k * RUN - H + j) * a.x_stride));
   }
 
-  float w[W][8], bias[8];
+  uint64_t w[W][4], bias[4];
   {
-    uint4 raw[W];
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      raw[j] = __ldg(reinterpret_cast<const uint4*>(a.weight + (int64_t)c0 * W) + j);
     float flat[W * 8];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      float f[8];
-      conv_unpack(raw[j], f);
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(a.weight + (int64_t)c0 * W) + j);
+      const uint32_t p[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) flat[j * 8 + i] = f[i];
+      for (int i = 0; i < 4; ++i) {
+        flat[j * 8 + 2 * i] = __uint_as_float(p[i] << 16);
+        flat[j * 8 + 2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[j][i] = flat[i * W + j];
-    if (a.bias) {
-      conv_unpack(__ldg(reinterpret_cast<const uint4*>(a.bias + c0)), bias);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) bias[i] = 0.f;
-    }
+      for (int j = 0; j < W; ++j) w[j][i] = f32x2(flat[2 * i * W + j], flat[(2 * i + 1) * W + j]);
+    conv_unpack(a.bias ? __ldg(reinterpret_cast<const uint4*>(a.bias + c0)) : make_uint4(0, 0, 0, 0),
+                bias);
   }
-  float win[W][8];  // win[W - 1]: the current row
+  uint64_t win[H][4];
 #pragma unroll
   for (int j = 0; j < H; ++j) conv_unpack(hist[j], win[j]);
 
@@ -122,31 +125,37 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
   const int rows = (int)(n - t0 < RUN ? n - t0 : RUN);
   __nv_bfloat16* out = a.out + (first + t0) * a.out_stride + c0;
   x += t0 * a.x_stride;
-  constexpr int kAhead = RUN < 4 ? RUN : 4;  // rows in flight per thread
+  // kAhead rows in flight per thread; a group of them shifts the window by renaming only
+  constexpr int kAhead = W == 3 ? 4 : 6;
+  static_assert(kAhead % H == 0, "a group of rows turns the window a whole number of times");
   for (int t = 0; t < rows; t += kAhead) {
     uint4 raw[kAhead];
 #pragma unroll
     for (int e = 0; e < kAhead; ++e)
-      if (t + e < rows) raw[e] = __ldg(reinterpret_cast<const uint4*>(x + (t + e) * a.x_stride));
+      if (t + e < rows) raw[e] = __ldcs(reinterpret_cast<const uint4*>(x + (t + e) * a.x_stride));
 #pragma unroll
     for (int e = 0; e < kAhead; ++e) {
       if (t + e >= rows) break;
-      conv_unpack(raw[e], win[H]);
-      float y[8];
+      uint64_t now[4];
+      conv_unpack(raw[e], now);
+      uint32_t packed[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = bias[i];
+      for (int i = 0; i < 4; ++i) {
+        uint64_t acc = bias[i];
 #pragma unroll
-        for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], win[j][i], y[i]);
-        if (a.silu) y[i] = __fdividef(y[i], 1.f + __expf(-y[i]));
+        for (int j = 0; j < H; ++j) acc = fma_f32x2(w[j][i], win[(e + j) % H][i], acc);
+        acc = fma_f32x2(w[H][i], now[i], acc);
+        float y0, y1;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(y0), "=f"(y1) : "l"(acc));
+        if (a.silu) {
+          y0 = __fdividef(y0, 1.f + __expf(-y0));
+          y1 = __fdividef(y1, 1.f + __expf(-y1));
+        }
+        packed[i] = pack_bf16x2(y0, y1);
+        win[e % H][i] = now[i];  // in the oldest row's place
       }
-      *reinterpret_cast<uint4*>(out + (t + e) * a.out_stride) =
-          make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                     pack_bf16x2(y[6], y[7]));
-#pragma unroll
-      for (int j = 0; j < H; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) win[j][i] = win[j + 1][i];
+      __stcs(reinterpret_cast<uint4*>(out + (t + e) * a.out_stride),
+             make_uint4(packed[0], packed[1], packed[2], packed[3]));
     }
   }
 }
