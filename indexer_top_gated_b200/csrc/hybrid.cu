@@ -60,6 +60,7 @@ int64_t row_stride(int64_t stride, int64_t width) {
 }
 
 // ---------------------------------------------------------------- rotary append
+// Turns per position of each pair.
 dsa_status rope_freqs(const dsa_rope_params* O, int rot, double* f) {
   if (rot == 0) return DSA_OK;
   long double theta = O->theta;
@@ -79,7 +80,7 @@ dsa_status rope_freqs(const dsa_rope_params* O, int rot, double* f) {
       x *= keep + (1 - keep) / O->factor;
     }
     if (!std::isfinite(x)) return DSA_ERR_INVALID_ARG;
-    f[i] = x;
+    f[i] = x / two_pi;
   }
   return DSA_OK;
 }
@@ -163,11 +164,11 @@ dsa_status dsa_rope_append(const dsa_params* P, const dsa_ragged* R, const dsa_r
     bool cache;
   };
   const Item items[5] = {
-      {&a.q, B->q, B->q_out, O->q_row_stride, P->n_q_heads, 128, false},
-      {&a.k, B->k, B->k_cache, O->k_row_stride, P->n_kv_heads, 128, true},
-      {&a.v, B->v, B->v_cache, O->v_row_stride, P->n_kv_heads, 128, true},
-      {&a.q_idx, B->q_idx, B->q_idx_out, O->q_idx_row_stride, P->n_idx_heads, 64, false},
-      {&a.k_idx, B->k_idx, B->k_idx_cache, O->k_idx_row_stride, P->n_idx_heads, 64, true}};
+      {&a.t[0], B->q, B->q_out, O->q_row_stride, P->n_q_heads, 128, false},
+      {&a.t[1], B->k, B->k_cache, O->k_row_stride, P->n_kv_heads, 128, true},
+      {&a.t[2], B->v, B->v_cache, O->v_row_stride, P->n_kv_heads, 128, true},
+      {&a.t[3], B->q_idx, B->q_idx_out, O->q_idx_row_stride, P->n_idx_heads, 64, false},
+      {&a.t[4], B->k_idx, B->k_idx_cache, O->k_idx_row_stride, P->n_idx_heads, 64, true}};
   Span in[5], out[5];
   for (int i = 0; i < 5; ++i) {
     const Item& t = items[i];
@@ -186,8 +187,8 @@ dsa_status dsa_rope_append(const dsa_params* P, const dsa_ragged* R, const dsa_r
                             out[i].bytes == in[i].bytes;
       if (!in_place) return DSA_ERR_INVALID_ARG;
     }
-  if (att) DSA_TRY(rope_freqs(O, O->rot_dim, a.freq));
-  if (idx) DSA_TRY(rope_freqs(O, O->idx_rot_dim, a.idx_freq));
+  if (att) DSA_TRY(rope_freqs(O, O->rot_dim, a.turns));
+  if (idx) DSA_TRY(rope_freqs(O, O->idx_rot_dim, a.idx_turns));
   a.q_offsets = R->q_offsets;
   a.kv_offsets = R->kv_offsets;
   a.positions = positions;
@@ -221,15 +222,19 @@ dsa_status dsa_rope_append(const dsa_params* P, const dsa_ragged* R, const dsa_r
 // ---------------------------------------------------------------- short convolution
 namespace dsa {
 namespace {
+constexpr int kConvRun = 48;  // rows of a run in a large batch
+
 template <int W>
 dsa_status launch_conv(const ConvArgs& a, const dsa_ragged* R, int sms, cudaStream_t st) {
   const int groups = (a.channels / 8 + kConvThreads - 1) / kConvThreads;
   // long runs read fewer rows twice; short ones spread a small batch over the GPU
-  const bool wide = R->total_q / 32 * groups >= 4 * (int64_t)sms;
-  const int64_t runs = R->total_q / (wide ? 32 : 8) + R->batch;
+  const bool wide = R->total_q / kConvRun * groups >= 4 * (int64_t)sms;
+  const bool single = R->max_q_len <= 1;
+  const int64_t runs = single ? R->batch : R->total_q / (wide ? kConvRun : 8) + R->batch;
   const unsigned y = (unsigned)std::min<int64_t>(runs, 32768);
   const dim3 grid((unsigned)groups, y, (unsigned)((runs + y - 1) / y));
-  if (wide) short_conv_kernel<W, 32><<<grid, kConvThreads, 0, st>>>(a);
+  if (single) short_conv_kernel<W, 1><<<grid, kConvThreads, 0, st>>>(a);
+  else if (wide) short_conv_kernel<W, kConvRun><<<grid, kConvThreads, 0, st>>>(a);
   else short_conv_kernel<W, 8><<<grid, kConvThreads, 0, st>>>(a);
   return launched("short_conv_kernel");
 }

@@ -18,10 +18,10 @@ constexpr int kRopePairs = 64;     // pairs of an attention head of 128, at most
 constexpr int kRopeIdxPairs = 32;  // pairs of an indexer head of 64, at most
 
 struct RopeTensor {
-  const __nv_bfloat16* src;  // nullptr: absent
+  const __nv_bfloat16* src;
   void* dst;
   int64_t src_stride;        // elements per packed row
-  int heads;
+  int heads;                 // 0: absent
 };
 
 struct RopeArgs {
@@ -30,40 +30,36 @@ struct RopeArgs {
   CachePages pg;
   int batch;
   int64_t total_q, cache_rows;
-  RopeTensor q, k, v, q_idx, k_idx;
+  RopeTensor t[5];           // q, k, v, q_idx, k_idx
   int32_t* err_count;
   int interleaved, idx_fp8;
   int rot, off, idx_rot, idx_off;
   float mscale, idx_scale_q, idx_scale_k;
-  double freq[kRopePairs], idx_freq[kRopeIdxPairs];
+  double turns[kRopePairs], idx_turns[kRopeIdxPairs];  // f_i / 2 pi
 };
 
-// Two 16-byte units (8 elements each) of a head of D elements, and how they turn.  Item t of a
-// head: the rotated units first (a pair's two halves, or two adjacent units of pairs), then the
-// units outside them.
+// Two 16-byte units (8 elements each) of a head of D elements, and the pairs they hold.  Item t
+// of a head: the rotated units first, then those outside them.  Both layouts take units half of
+// the part apart (the two halves of eight pairs, or four pairs each), so that neighbouring
+// threads touch neighbouring units: whole sectors.
 struct RopeItem {
-  int u0, u1;  // units
-  int pair0;   // first pair of unit u0, -1: not rotated
+  int u0, u1;        // units
+  int pair0, pair1;  // pairs of c[0 .. 3] and c[4 .. 7]; pair0 -1: not rotated
 };
 template <int D>
 DSA_DEV RopeItem rope_item(int t, int rot, int off, bool interleaved) {
   RopeItem it;
   const int turned = rot >> 4, o = off >> 3;
   if (t < turned) {
-    if (interleaved) {
-      it.u0 = o + 2 * t;
-      it.u1 = it.u0 + 1;
-    } else {
-      it.u0 = o + t;
-      it.u1 = it.u0 + turned;
-    }
-    it.pair0 = t * 8;
+    it.u0 = o + t;
+    it.u1 = it.u0 + turned;
+    it.pair0 = interleaved ? t * 4 : t * 8;
+    it.pair1 = interleaved ? (t + turned) * 4 : t * 8 + 4;
   } else {
-    int j = (t - turned) * 2;
+    const int j = t - turned, k = j + D / 16 - turned;
     it.u0 = j < o ? j : j + 2 * turned;
-    ++j;
-    it.u1 = j < o ? j : j + 2 * turned;
-    it.pair0 = -1;
+    it.u1 = k < o ? k : k + 2 * turned;
+    it.pair0 = it.pair1 = -1;
   }
   return it;
 }
@@ -77,8 +73,8 @@ DSA_DEV void rope_unpack(uint4 x, float (&f)[8]) {
   }
 }
 
-// Turns the item's elements: a = unit u0, b = unit u1, cs = cos and sin of the row's pairs.
-DSA_DEV void rope_turn(float (&a)[8], float (&b)[8], const float2* cs, bool interleaved) {
+// Turns the item's elements: a = unit u0, b = unit u1, cs = cos and sin of its eight pairs.
+DSA_DEV void rope_turn(float (&a)[8], float (&b)[8], const float2 (&cs)[8], bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -93,10 +89,9 @@ DSA_DEV void rope_turn(float (&a)[8], float (&b)[8], const float2* cs, bool inte
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 c = cs[i];
       const float x = a[i], y = b[i];
-      a[i] = x * c.x - y * c.y;
-      b[i] = x * c.y + y * c.x;
+      a[i] = x * cs[i].x - y * cs[i].y;
+      b[i] = x * cs[i].y + y * cs[i].x;
     }
   }
 }
@@ -121,57 +116,86 @@ DSA_DEV void rope_store_fp8(unsigned char* dst, const float (&f)[8], float scale
   *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
 
-// All items of one tensor over the CTA's rows.  dst row of row i: rows[i] (-1: not written).
-template <int D, bool kRotate, bool kIdx>
-DSA_DEV void rope_tensor(const RopeArgs& a, const RopeTensor& x, int64_t r0, int n,
-                         const int64_t* rows, const float2* cs, int cs_ld, float scale) {
-  if (!x.src) return;
-  const int per_row = x.heads * (D / 16);
-  const int rot = !kRotate ? 0 : kIdx ? a.idx_rot : a.rot;
-  const int off = kIdx ? a.idx_off : a.off;
-  const bool inter = a.interleaved != 0;
-#pragma unroll 2
-  for (int at = threadIdx.x; at < n * per_row; at += kRopeThreads) {
-    const int i = at / per_row, rem = at - i * per_row;
-    const int h = rem / (D / 16);
-    const RopeItem it = rope_item<D>(rem % (D / 16), rot, off, inter);
-    const int64_t row = rows[i];
-    if (row < 0) continue;
-    const __nv_bfloat16* src = x.src + (r0 + i) * x.src_stride + h * D;
-    const uint4 u = *reinterpret_cast<const uint4*>(src + it.u0 * 8);
-    const uint4 w = *reinterpret_cast<const uint4*>(src + it.u1 * 8);
-    const int64_t to = (row * x.heads + h) * D;
-    if (it.pair0 < 0 && !(kIdx && a.idx_fp8)) {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(x.dst) + to;
-      *reinterpret_cast<uint4*>(dst + it.u0 * 8) = u;
-      *reinterpret_cast<uint4*>(dst + it.u1 * 8) = w;
-      continue;
-    }
-    float f[8], g[8];
-    rope_unpack(u, f);
-    rope_unpack(w, g);
-    if (it.pair0 >= 0) rope_turn(f, g, cs + i * cs_ld + it.pair0, inter);
-    if (kIdx && a.idx_fp8) {
-      unsigned char* dst = static_cast<unsigned char*>(x.dst) + to;
-      rope_store_fp8(dst + it.u0 * 8, f, scale);
-      rope_store_fp8(dst + it.u1 * 8, g, scale);
-    } else {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(x.dst) + to;
-      rope_store_bf16(dst + it.u0 * 8, f);
-      rope_store_bf16(dst + it.u1 * 8, g);
-    }
+DSA_DEV void rope_pairs(float2 (&c)[8], const float2* row, const RopeItem& it) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    c[j] = it.pair0 < 0 ? make_float2(1.f, 0.f) : row[it.pair0 + j];
+    c[4 + j] = it.pair0 < 0 ? make_float2(1.f, 0.f) : row[it.pair1 + j];
   }
 }
 
-// ROWS consecutive packed rows per CTA.
+// One item of a head in registers: turned if it is a rotated one, then stored at element `to` of
+// the output.
+DSA_DEV void rope_finish(const RopeTensor& x, int64_t to, const RopeItem& it, uint4 u, uint4 w,
+                         bool turn, const float2 (&cs)[8], bool inter, bool fp8, float scale) {
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(x.dst) + to;
+  if (!turn && !fp8) {
+    *reinterpret_cast<uint4*>(dst + it.u0 * 8) = u;
+    *reinterpret_cast<uint4*>(dst + it.u1 * 8) = w;
+    return;
+  }
+  float f[8], g[8];
+  rope_unpack(u, f);
+  rope_unpack(w, g);
+  if (turn) rope_turn(f, g, cs, inter);
+  if (fp8) {
+    unsigned char* d8 = static_cast<unsigned char*>(x.dst) + to;
+    rope_store_fp8(d8 + it.u0 * 8, f, scale);
+    rope_store_fp8(d8 + it.u1 * 8, g, scale);
+  } else {
+    rope_store_bf16(dst + it.u0 * 8, f);
+    rope_store_bf16(dst + it.u1 * 8, g);
+  }
+}
+
+// ROWS consecutive packed rows per CTA, 256 / ROWS threads a row.  A thread keeps one item of a
+// head and steps over the heads of q, k and v (one list), then those of q_idx and k_idx.  Its
+// copies go through its own slots of a ring in shared memory, kRopeAhead items in flight, and the
+// first are under way before the row's sequence and angles are known: the kernel is bound by how
+// much it keeps in flight, and registers would hold less.
+constexpr int kRopeAhead = 4;
+
 template <int ROWS>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ uint4 ring[kRopeAhead + 1][2][kRopeThreads];
   __shared__ float2 cs[ROWS][kRopePairs], ics[ROWS][kRopeIdxPairs];
   __shared__ int64_t q_rows[ROWS], c_rows[ROWS];
   __shared__ int pos[ROWS];
   const int tid = threadIdx.x;
   const int64_t r0 = (int64_t)blockIdx.x * ROWS;
   const int n = (int)(a.total_q - r0 < ROWS ? a.total_q - r0 : ROWS);
+  constexpr int kThreads = kRopeThreads / ROWS, kHeads = kThreads / 8, kIdxHeads = kThreads / 4;
+  const int my = tid / kThreads, t = tid % kThreads;
+  const int64_t row = r0 + my;
+  const bool inter = a.interleaved != 0;
+  const int nq = a.t[0].heads, nk = nq + a.t[1].heads, heads = my < n ? nk + a.t[2].heads : 0;
+  const int ni = a.t[3].heads, idx_heads = my < n ? ni + a.t[4].heads : 0;
+  const RopeItem it = rope_item<128>(t % 8, a.rot, a.off, inter);
+  const RopeItem iit = rope_item<64>(t % 4, a.idx_rot, a.idx_off, inter);
+
+  // head vh of the list q, k, v (an absent tensor has no heads)
+  auto source = [&](int vh) {
+    const RopeTensor& x = a.t[vh < nq ? 0 : vh < nk ? 1 : 2];
+    return x.src + row * x.src_stride + (vh - (vh < nq ? 0 : vh < nk ? nq : nk)) * 128;
+  };
+  auto idx_source = [&](int vh) {
+    const RopeTensor& x = a.t[vh < ni ? 3 : 4];
+    return x.src + row * x.src_stride + (vh < ni ? vh : vh - ni) * 64;
+  };
+  const uint32_t slot = smem_u32(&ring[0][0][tid]);
+  constexpr uint32_t kHalf = sizeof(ring[0][0]), kSlot = sizeof(ring[0]);
+  auto fetch = [&](uint32_t to, const __nv_bfloat16* src, const RopeItem& i) {
+    cp_async_16(to, src + i.u0 * 8, 16);
+    cp_async_16(to + kHalf, src + i.u1 * 8, 16);
+  };
+  if (t / 4 < idx_heads) fetch(slot + kRopeAhead * kSlot, idx_source(t / 4), iit);
+#pragma unroll
+  for (int e = 0; e < kRopeAhead; ++e) {
+    const int vh = t / 8 + e * kHeads;
+    if (vh < heads) fetch(slot + e * kSlot, source(vh), it);
+    cp_async_commit();
+  }
+
   const int b0 = seq_of_row_cta<kRopeThreads>(a.q_offsets, a.batch, r0);
   if (tid < n) {
     const int64_t r = r0 + tid;
@@ -204,21 +228,55 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const int n_att = a.rot >> 1, n_idx = a.idx_rot >> 1, per = n_att + n_idx;
   for (int at = tid; at < n * per; at += kRopeThreads) {
     const int i = at / per, j = at - i * per;
-    const double f = j < n_att ? a.freq[j] : a.idx_freq[j - n_att];
-    double x = (double)pos[i] * f;
-    x -= rint(x * 0.15915494309189533577) * 6.283185307179586477;
+    const double x = (double)pos[i] * (j < n_att ? a.turns[j] : a.idx_turns[j - n_att]);
     float s, c;
-    sincosf((float)x, &s, &c);
+    sincospif(2.f * (float)(x - rint(x)), &s, &c);
     const float2 v = make_float2(c * a.mscale, s * a.mscale);
     if (j < n_att) cs[i][j] = v;
     else ics[i][j - n_att] = v;
   }
   __syncthreads();
-  rope_tensor<128, true, false>(a, a.q, r0, n, q_rows, &cs[0][0], kRopePairs, 1.f);
-  rope_tensor<128, true, false>(a, a.k, r0, n, c_rows, &cs[0][0], kRopePairs, 1.f);
-  rope_tensor<128, false, false>(a, a.v, r0, n, c_rows, &cs[0][0], kRopePairs, 1.f);
-  rope_tensor<64, true, true>(a, a.q_idx, r0, n, q_rows, &ics[0][0], kRopeIdxPairs, a.idx_scale_q);
-  rope_tensor<64, true, true>(a, a.k_idx, r0, n, c_rows, &ics[0][0], kRopeIdxPairs, a.idx_scale_k);
+  if (my >= n) return;
+  const int64_t q_row = q_rows[my], c_row = c_rows[my];
+  float2 c[8];
+  rope_pairs(c, cs[my], it);
+  const uint4* mine = &ring[0][0][tid];
+#pragma unroll 1
+  for (int vh = t / 8; vh < heads; vh += kRopeAhead * kHeads) {
+#pragma unroll
+    for (int e = 0; e < kRopeAhead; ++e) {
+      cp_async_wait<kRopeAhead - 1>();
+      const uint4 u = mine[e * 2 * kRopeThreads], w = mine[(e * 2 + 1) * kRopeThreads];
+      const int now = vh + e * kHeads, next = now + kRopeAhead * kHeads;
+      if (next < heads) fetch(slot + e * kSlot, source(next), it);
+      cp_async_commit();
+      if (now >= heads) continue;
+      const RopeTensor& x = a.t[now < nq ? 0 : now < nk ? 1 : 2];
+      const int h = now - (now < nq ? 0 : now < nk ? nq : nk);
+      const int64_t to = now < nq ? q_row : c_row;
+      if (to >= 0)
+        rope_finish(x, (to * x.heads + h) * 128, it, u, w, now < nk && it.pair0 >= 0, c, inter,
+                    false, 1.f);
+    }
+  }
+  rope_pairs(c, ics[my], iit);
+  for (int vh = t / 4; vh < idx_heads; vh += kIdxHeads) {
+    uint4 u, w;
+    if (vh == t / 4) {
+      cp_async_wait<0>();
+      u = mine[kRopeAhead * 2 * kRopeThreads], w = mine[(kRopeAhead * 2 + 1) * kRopeThreads];
+    } else {
+      const __nv_bfloat16* src = idx_source(vh);
+      u = *reinterpret_cast<const uint4*>(src + iit.u0 * 8);
+      w = *reinterpret_cast<const uint4*>(src + iit.u1 * 8);
+    }
+    const bool first = vh < ni;
+    const RopeTensor& x = a.t[first ? 3 : 4];
+    const int64_t to = first ? q_row : c_row;
+    if (to >= 0)
+      rope_finish(x, (to * x.heads + (first ? vh : vh - ni)) * 64, iit, u, w,
+                  iit.pair0 >= 0, c, inter, a.idx_fp8, first ? a.idx_scale_q : a.idx_scale_k);
+  }
 }
 
 }  // namespace dsa

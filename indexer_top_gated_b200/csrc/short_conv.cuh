@@ -52,16 +52,21 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
   const int c0 = (blockIdx.x * kConvThreads + threadIdx.x) * 8;
   const int64_t run = (int64_t)blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
   int b = 0;
-  for (int i = 1; i < a.batch; i += kConvThreads) {
-    const int at = i + threadIdx.x;
-    b += __syncthreads_count(at < a.batch && __ldg(a.q_offsets + at) / RUN + at <= run);
+  if (RUN == 1) {  // single tokens: run b is sequence b
+    if (run >= a.batch) return;
+    b = (int)run;
+  } else {
+    for (int i = 1; i < a.batch; i += kConvThreads) {
+      const int at = i + threadIdx.x;
+      b += __syncthreads_count(at < a.batch && __ldg(a.q_offsets + at) / RUN + at <= run);
+    }
   }
   if (c0 >= a.channels) return;
   const int64_t first = __ldg(a.q_offsets + b);
   const int64_t n = __ldg(a.q_offsets + b + 1) - first;
-  const int64_t k = run - (first / RUN + b);
-  if (k > 0 && k * RUN >= n) return;
+  const int64_t k = RUN == 1 ? 0 : run - (first / RUN + b);
   constexpr int H = W - 1;
+  if (k > 0 && k * RUN >= n) return;
   const __nv_bfloat16* x = a.x + first * a.x_stride + c0;
 
   uint4 hist[H];  // the H rows before the run, oldest first
@@ -125,19 +130,30 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
   const int rows = (int)(n - t0 < RUN ? n - t0 : RUN);
   __nv_bfloat16* out = a.out + (first + t0) * a.out_stride + c0;
   x += t0 * a.x_stride;
-  // kAhead rows in flight per thread; a group of them shifts the window by renaming only
-  constexpr int kAhead = W == 3 ? 4 : 6;
-  static_assert(kAhead % H == 0, "a group of rows turns the window a whole number of times");
-  for (int t = 0; t < rows; t += kAhead) {
-    uint4 raw[kAhead];
+  // A ring of rows in shared memory keeps kGroup of them in flight without holding registers.  A
+  // thread reads back only what it copied itself: no barrier.  A group of rows turns ring and
+  // window a whole number of times, so both are indexed by constants.
+  constexpr int kGroup = RUN == 1 ? 1 : H == 3 ? 6 : 8;
+  __shared__ uint4 ring[kGroup][kConvThreads];
+  const uint4* mine = &ring[0][threadIdx.x];
+  const uint32_t slot = smem_u32(mine);
+  const int64_t x_step = a.x_stride, out_step = a.out_stride;
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e)
-      if (t + e < rows) raw[e] = __ldcs(reinterpret_cast<const uint4*>(x + (t + e) * a.x_stride));
+  for (int e = 0; e < kGroup; ++e) {
+    if (e < rows) cp_async_16(slot + e * sizeof(ring[0]), x, 16);
+    cp_async_commit();
+    x += x_step;
+  }
+#pragma unroll 1
+  for (int left = rows; left > 0; left -= kGroup) {
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      if (t + e >= rows) break;
+    for (int e = 0; e < kGroup; ++e) {
+      cp_async_wait<kGroup - 1>();
       uint64_t now[4];
-      conv_unpack(raw[e], now);
+      conv_unpack(mine[e * kConvThreads], now);
+      if (e + kGroup < left) cp_async_16(slot + e * sizeof(ring[0]), x, 16);
+      cp_async_commit();
+      x += x_step;
       uint32_t packed[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -148,14 +164,22 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
         float y0, y1;
         asm("mov.b64 {%0, %1}, %2;" : "=f"(y0), "=f"(y1) : "l"(acc));
         if (a.silu) {
-          y0 = __fdividef(y0, 1.f + __expf(-y0));
-          y1 = __fdividef(y1, 1.f + __expf(-y1));
+          // y / (1 + e^-y) of both by one reciprocal; 2^58 already leaves nothing of y, and its
+          // square is finite
+          constexpr float kLog2e = 1.44269504f;
+          const float d0 = 1.f + ex2_approx(fminf(-kLog2e * y0, 58.f));
+          const float d1 = 1.f + ex2_approx(fminf(-kLog2e * y1, 58.f));
+          const float r = __fdividef(1.f, d0 * d1);
+          y0 *= d1 * r;
+          y1 *= d0 * r;
         }
         packed[i] = pack_bf16x2(y0, y1);
         win[e % H][i] = now[i];  // in the oldest row's place
       }
-      __stcs(reinterpret_cast<uint4*>(out + (t + e) * a.out_stride),
-             make_uint4(packed[0], packed[1], packed[2], packed[3]));
+      if (e < left)
+        __stcs(reinterpret_cast<uint4*>(out),
+               make_uint4(packed[0], packed[1], packed[2], packed[3]));
+      out += out_step;
     }
   }
 }
