@@ -52,6 +52,7 @@ struct DeltaArgs {
   // chunked form
   unsigned char* ws;     // kDeltaItemBytes per (chunk slot, head of the pass)
   int head0, heads;      // heads of the pass
+  int per_cta;           // value heads of a preparation CTA (of one key head)
   int* status;           // device status word
 };
 
@@ -252,7 +253,8 @@ DSA_DEV void split_frag(const float (&x)[4], const float (&y)[4], uint32_t (&f)[
 
 // ------------------------------------------------------------------ chunked form: T and P
 //
-// One CTA per (chunk, value head).  Each of its four warps forms 16 rows of K K^T and Q K^T up
+// One CTA per chunk and one value head, or all value heads of one key head (K K^T and Q K^T are
+// theirs in common).  Each of its four warps forms 16 rows of K K^T and Q K^T up
 // to the diagonal (they share K's operands and the decays); then I + A is inverted in place, in
 // fp32: its 16 x 16 diagonal blocks by forward substitution, and the blocks below by
 //   [T1 0; -T2 A21 T1, T2], twice, 16 -> 32 -> 64.
@@ -296,12 +298,15 @@ DSA_DEV void prep_mma(float (&acc)[4], const uint32_t (&x)[3][4], const uint32_t
     for (int py = 0; py < 3 - px; ++py) mma_bf16_16816(acc, x[px], y[py][0], y[py][1]);
 }
 
-// Y [16 columns of T1][8 NT rows of A21] += T1^T A21^T over 16 KT rows of T1
-template <int KT, int NT>
-DSA_DEV void prep_product(const float* T1, const float* A21, float (&y)[NT][4]) {
+// Y [16 columns of T1][rows of A21, eight each] += T1^T A21^T over the 16-row tiles kt0 .. kt1-1
+// of T1; the first `nts` row tiles of A21.  (A loop over kt: unrolled, it is bound by instruction
+// fetch.)
+template <int NT>
+DSA_DEV void prep_product(const float* T1, const float* A21, int kt0, int kt1, int nts,
+                          float (&y)[NT][4]) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll 1
+  for (int kt = kt0; kt < kt1; ++kt) {
     uint32_t fx[3][4], p[3];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // (m, k), (m + 8, k), (m, k + 8), (m + 8, k + 8)
@@ -312,6 +317,7 @@ DSA_DEV void prep_product(const float* T1, const float* A21, float (&y)[NT][4]) 
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      if (nt >= nts) break;
       uint32_t fb[3][2];
       prep_right(A21 + nt * 8 * kPrepLd + kt * 16, fb);
       prep_mma(y[nt], fx, fb);
@@ -329,14 +335,15 @@ DSA_DEV void prep_store(float* T21, const float (&t)[4]) {
   at[kPrepLd + 8] = -t[3];
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
+template <bool kGroup>
+__global__ void __launch_bounds__(kPrepThreads, kGroup ? 4 : 5) delta_prep_kernel(
     const DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t item = blockIdx.x;
-  const int64_t slot = item / a.heads;
-  const int h = a.head0 + (int)(item % a.heads);
+  const int groups = kGroup ? a.heads / a.per_cta : a.heads;
+  const int64_t slot = blockIdx.x / groups;
+  const int hl0 = (int)(blockIdx.x % groups) * (kGroup ? a.per_cta : 1);  // first of its value heads
   int lo = 0;  // the sequence whose slots hold this one
   for (int i = 1; i < a.batch; i += kPrepThreads)
     lo += __syncthreads_count(i + tid < a.batch && delta_first_slot(a, i + tid) <= slot);
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
   const int64_t row0 = first + (slot - delta_first_slot(a, lo)) * kDeltaChunk;
   if (end - first < a.min_len || row0 >= end) return;
   const int valid = (int)(end - row0 < kDeltaChunk ? end - row0 : kDeltaChunk);
-  const int hk = h / (a.hv / a.hk);
+  const int hk = (a.head0 + hl0) / (a.hv / a.hk);
 
   const uint32_t sk = smem_u32(sm.k), sq = smem_u32(sm.q);
   const uint32_t bar = smem_u32(&sm.bar);
@@ -355,36 +362,39 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
     mbar_arrive_expect_tx(bar, 2 * kDeltaTile);
     delta_load_qk(maps, sk, sq, bar, hk, row0);
   }
-  if (warp == 0) {
-    // running sum of g, two tokens a lane, in fp64 and then as a pair of fp32.  -inf (alpha = 0)
-    // becomes a finite decay that is 0 all the same, so that differences of sums behind it stay
-    // numbers.
-    double x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = lane * 2 + i;
-      const float g = t < valid ? __ldg(a.g + (row0 + t) * a.hv + h) : 0.f;
-      x[i] = g < -1e5f ? -1e5 : (double)g;
+  auto gates = [&](int h) {
+    if (warp == 0) {
+      // running sum of g, two tokens a lane, in fp64 and then as a pair of fp32.  -inf (alpha = 0)
+      // becomes a finite decay that is 0 all the same, so that differences of sums behind it stay
+      // numbers.
+      double x[2];
+  #pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = lane * 2 + i;
+        const float g = t < valid ? __ldg(a.g + (row0 + t) * a.hv + h) : 0.f;
+        x[i] = g < -1e5f ? -1e5 : (double)g;
+      }
+      double sum = x[0] + x[1];
+      const double own = sum;
+  #pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const double up = __shfl_up_sync(~0u, sum, m);
+        if (lane >= m) sum += up;
+      }
+      const double first_of_two = sum - own + x[0];
+      float f = (float)first_of_two;
+      sm.G[lane * 2] = make_float2(f, (float)(first_of_two - f));
+      f = (float)sum;
+      sm.G[lane * 2 + 1] = make_float2(f, (float)(sum - f));
+    } else if (warp == 1) {
+  #pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = lane + i * 32;
+        sm.beta[t] = t < valid ? __ldg(a.beta + (row0 + t) * a.hv + h) : 0.f;
+      }
     }
-    double sum = x[0] + x[1];
-    const double own = sum;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const double up = __shfl_up_sync(~0u, sum, m);
-      if (lane >= m) sum += up;
-    }
-    const double first_of_two = sum - own + x[0];
-    float f = (float)first_of_two;
-    sm.G[lane * 2] = make_float2(f, (float)(first_of_two - f));
-    f = (float)sum;
-    sm.G[lane * 2 + 1] = make_float2(f, (float)(sum - f));
-  } else if (warp == 1) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = lane + i * 32;
-      sm.beta[t] = t < valid ? __ldg(a.beta + (row0 + t) * a.hv + h) : 0.f;
-    }
-  }
+  };
+  gates(a.head0 + hl0);
   __syncthreads();  // the barrier is there to wait for
   mbar_wait_bounded(bar, 0, a.status, &sm.abort);
   if (valid < kDeltaChunk) {
@@ -412,9 +422,9 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
   }
 
   // rows of 16 tokens (tile mt) of K K^T and Q K^T, columns up to the diagonal tile.  The tiles
-  // turn with the item, so that the longest is not always on the same scheduler.
+  // turn with the CTA, so that the longest is not always on the same scheduler.
   const int mi = lane >> 3, mr = lane & 7;
-  const int mt = (warp + (int)(item & 3)) & 3;
+  const int mt = (warp + (int)(blockIdx.x & 3)) & 3;
   float kk[8][4], qk[8][4];
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt)
@@ -437,9 +447,12 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
       }
     }
   }
-  __syncthreads();  // the norms are there; K's and Q's tiles are free
+  const int per = kGroup ? a.per_cta : 1;
+#pragma unroll 1
+  for (int hl = hl0; hl < hl0 + per; ++hl) {
+  __syncthreads();  // gates and norms are there; K's and Q's tiles, or the last head's A, are free
 
-  unsigned char* dst = a.ws + item * kDeltaItemBytes;
+  unsigned char* dst = a.ws + (slot * a.heads + hl) * kDeltaItemBytes;
   if (tid < 64) {
     float* scal = reinterpret_cast<float*>(dst + kDeltaScal);
     const float2 g = sm.G[tid], ge = sm.G[63];
@@ -524,7 +537,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
     float* T1 = sm.A + part * 32 * (kPrepLd + 1);
     float* A21 = T1 + 16 * kPrepLd;
     float y[2][4] = {}, t[4] = {};
-    prep_product<1, 2>(T1, A21, y);
+    prep_product<2>(T1, A21, 0, 1, 2, y);
     uint32_t fy[3][4], fb[3][2];
     split_frag<3>(y[0], y[1], fy);
     prep_right(A21 + 16 + half * 8 * kPrepLd, fb);
@@ -536,11 +549,11 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
   {  // columns 16 part .. of the 32 x 32 block below, rows 16 half ..
     float* A21 = sm.A + 32 * kPrepLd;
     float y[4][4] = {}, t[2][4] = {};
-    if (part) prep_product<1, 4>(sm.A + 16 * (kPrepLd + 1), A21 + 16, y);
-    else prep_product<2, 4>(sm.A, A21, y);
+    // T1 and T2 are lower triangular: rows 16 part .. of T1, and the first 16 (half + 1) of Y
+    prep_product<4>(sm.A + part * 16, A21, part, 2, 2 * (half + 1), y);
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      if (kt > half) continue;  // T2 is lower triangular
+      if (kt > half) continue;
       uint32_t fy[3][4];
       split_frag<3>(y[2 * kt], y[2 * kt + 1], fy);
 #pragma unroll
@@ -572,6 +585,11 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prep_kernel(
     for (int m = 0; m < 3; ++m)
       *reinterpret_cast<uint4*>(dst + m * kDeltaMat + tri_unit(i, c)) =
           make_uint4(p[0][m], p[1][m], p[2][m], p[3][m]);
+  }
+  if (kGroup && hl + 1 < hl0 + per) {
+    __syncthreads();
+    gates(a.head0 + hl + 1);
+  }
   }
 }
 

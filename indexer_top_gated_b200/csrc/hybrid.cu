@@ -97,7 +97,8 @@ cudaError_t hybrid_allow_smem() {
   auto allow = [](const void* f, int bytes) {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  cudaError_t e = allow((const void*)delta_prep_kernel, (int)sizeof(PrepSmem));
+  cudaError_t e = allow((const void*)delta_prep_kernel<false>, (int)sizeof(PrepSmem));
+  e = e ? e : allow((const void*)delta_prep_kernel<true>, (int)sizeof(PrepSmem));
   e = e ? e : allow((const void*)delta_scan_kernel, kScanSmem);
   return e;
 }
@@ -429,7 +430,15 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   for (int h0 = 0; h0 < a.hv; h0 += (int)pass) {
     a.head0 = h0;
     a.heads = (int)std::min<int64_t>(pass, a.hv - h0);
-    delta_prep_kernel<<<(unsigned)(slots * a.heads), kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
+    // value heads of one key head together, where a pass is whole groups of them and CTAs abound
+    const int group = a.hv / a.hk;
+    const bool whole = h0 % group == 0 && a.heads % group == 0;
+    a.per_cta = whole && slots * (a.heads / group) >= 8 * (int64_t)dev.num_sms ? group : 1;
+    const unsigned ctas = (unsigned)(slots * (a.heads / a.per_cta));
+    if (a.per_cta > 1)
+      delta_prep_kernel<true><<<ctas, kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
+    else
+      delta_prep_kernel<false><<<ctas, kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
     DSA_TRY(launched("delta_prep_kernel"));
     DSA_TRY(launch_scan(a, maps, st));
   }
