@@ -28,6 +28,8 @@
 // bf16: P enters rounded once and U with two pieces, an error no larger than that rounding's.
 #pragma once
 
+#include <cstddef>
+
 #include "common.cuh"
 
 namespace dsa {
@@ -254,8 +256,8 @@ DSA_DEV void split_frag(const float (&x)[4], const float (&y)[4], uint32_t (&f)[
 // ------------------------------------------------------------------ chunked form: T and P
 //
 // One CTA per chunk and one value head, or all value heads of one key head (K K^T and Q K^T are
-// theirs in common).  Each of its four warps forms 16 rows of K K^T and Q K^T up
-// to the diagonal (they share K's operands and the decays); then I + A is inverted in place, in
+// theirs in common).  Its four warps form K K^T and Q K^T on and below the
+// diagonal (they share K's operands and the decays); then I + A is inverted in place, in
 // fp32: its 16 x 16 diagonal blocks by forward substitution, and the blocks below by
 //   [T1 0; -T2 A21 T1, T2], twice, 16 -> 32 -> 64.
 // Written as loops rather than one unrolled substitution over 64 rows: that was bound by
@@ -270,11 +272,14 @@ struct PrepSmem {
     };
     float A[kDeltaChunk * kPrepLd];  // once the products are in registers
   };
+  alignas(16) float2 G[kDeltaChunk];  // running sum of g, high and low part
+  alignas(16) float ink[kDeltaChunk], inq[kDeltaChunk], beta[kDeltaChunk];
   uint64_t bar;
   int abort;
-  float2 G[kDeltaChunk];  // running sum of g, high and low part
-  float ink[kDeltaChunk], inq[kDeltaChunk], beta[kDeltaChunk];
 };
+static_assert(offsetof(PrepSmem, G) % 16 == 0 && offsetof(PrepSmem, inq) % 16 == 0 &&
+                  offsetof(PrepSmem, beta) % 16 == 0,
+              "read 16 bytes at a time");
 
 // Pieces of the right operand X^T (k = column of X, n = row of X) of eight rows, 16 columns.
 DSA_DEV void prep_right(const float* X, uint32_t (&f)[3][2]) {
@@ -290,38 +295,28 @@ DSA_DEV void prep_right(const float* X, uint32_t (&f)[3][2]) {
   }
 }
 
-// acc += the product of two operands in three pieces each
-DSA_DEV void prep_mma(float (&acc)[4], const uint32_t (&x)[3][4], const uint32_t (&y)[3][2]) {
+// y[i] += the products of x with N right operands, in three pieces each; the accumulators take
+// turns
+template <int N>
+DSA_DEV void prep_mma(float (&y)[N][4], const uint32_t (&x)[3][4], const uint32_t (&f)[N][3][2]) {
 #pragma unroll
   for (int px = 0; px < 3; ++px)
 #pragma unroll
-    for (int py = 0; py < 3 - px; ++py) mma_bf16_16816(acc, x[px], y[py][0], y[py][1]);
+    for (int py = 0; py < 3 - px; ++py)
+#pragma unroll
+      for (int i = 0; i < N; ++i) mma_bf16_16816(y[i], x[px], f[i][py][0], f[i][py][1]);
 }
 
-// Y [16 columns of T1][rows of A21, eight each] += T1^T A21^T over the 16-row tiles kt0 .. kt1-1
-// of T1; the first `nts` row tiles of A21.  (A loop over kt: unrolled, it is bound by instruction
-// fetch.)
-template <int NT>
-DSA_DEV void prep_product(const float* T1, const float* A21, int kt0, int kt1, int nts,
-                          float (&y)[NT][4]) {
+// Pieces of T1^T: 16 columns of T1 from column 0, its 16 rows from row 0
+DSA_DEV void prep_left(const float* T1, uint32_t (&fx)[3][4]) {
   const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int kt = kt0; kt < kt1; ++kt) {
-    uint32_t fx[3][4], p[3];
+  uint32_t p[3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // (m, k), (m + 8, k), (m, k + 8), (m + 8, k + 8)
-      const float* at = T1 + (kt * 16 + (lane & 3) * 2 + (i >> 1) * 8) * kPrepLd + (lane >> 2) + (i & 1) * 8;
-      split_pair<3>(at[0], at[kPrepLd], p);
+  for (int i = 0; i < 4; ++i) {  // (m, k), (m + 8, k), (m, k + 8), (m + 8, k + 8)
+    const float* at = T1 + ((lane & 3) * 2 + (i >> 1) * 8) * kPrepLd + (lane >> 2) + (i & 1) * 8;
+    split_pair<3>(at[0], at[kPrepLd], p);
 #pragma unroll
-      for (int m = 0; m < 3; ++m) fx[m][i] = p[m];
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt >= nts) break;
-      uint32_t fb[3][2];
-      prep_right(A21 + nt * 8 * kPrepLd + kt * 16, fb);
-      prep_mma(y[nt], fx, fb);
-    }
+    for (int m = 0; m < 3; ++m) fx[m][i] = p[m];
   }
 }
 
@@ -336,7 +331,7 @@ DSA_DEV void prep_store(float* T21, const float (&t)[4]) {
 }
 
 template <bool kGroup>
-__global__ void __launch_bounds__(kPrepThreads, kGroup ? 4 : 5) delta_prep_kernel(
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
     const DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(smem_raw);
@@ -405,7 +400,7 @@ __global__ void __launch_bounds__(kPrepThreads, kGroup ? 4 : 5) delta_prep_kerne
   {
     const int r = tid & 63;
     const unsigned char* tile = tid < 64 ? sm.k : sm.q;
-    float ss = 0.f;
+    float ss[4] = {0.f, 0.f, 0.f, 0.f};
     if (a.norm) {
 #pragma unroll 4
       for (int c = 0; c < 16; ++c) {
@@ -413,37 +408,57 @@ __global__ void __launch_bounds__(kPrepThreads, kGroup ? 4 : 5) delta_prep_kerne
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          ss = fmaf(bf16_lo(w[i]), bf16_lo(w[i]), ss);
-          ss = fmaf(bf16_hi(w[i]), bf16_hi(w[i]), ss);
+          ss[i] = fmaf(bf16_lo(w[i]), bf16_lo(w[i]), ss[i]);
+          ss[i] = fmaf(bf16_hi(w[i]), bf16_hi(w[i]), ss[i]);
         }
       }
     }
-    (tid < 64 ? sm.ink : sm.inq)[r] = a.norm ? 1.f / sqrtf(ss + a.eps) : 1.f;
+    (tid < 64 ? sm.ink : sm.inq)[r] = 
+        a.norm ? 1.f / sqrtf((ss[0] + ss[1]) + (ss[2] + ss[3]) + a.eps) : 1.f;
   }
 
-  // rows of 16 tokens (tile mt) of K K^T and Q K^T, columns up to the diagonal tile.  The tiles
-  // turn with the CTA, so that the longest is not always on the same scheduler.
+  // K K^T and Q K^T on and below the diagonal: twenty tiles of 16 rows and 8 columns, five to a
+  // warp: (row tile, column tile) from (3, 0), from (3, 5) and (0, 0), from (2, 0), from (2, 5)
+  // and (1, 0).  The roles turn with the CTA, so that none is always on the same scheduler.
   const int mi = lane >> 3, mr = lane & 7;
-  const int mt = (warp + (int)(blockIdx.x & 3)) & 3;
-  float kk[8][4], qk[8][4];
+  const int role = (warp + (int)(blockIdx.x & 3)) & 3;
+  const int mt_a = 3 - (role >> 1), mt_b = role >> 1;                // row tiles
+  const int n_a = role & 1 ? (role == 1 ? 3 : 1) : 5;                // column tiles of mt_a
+  const int nt0 = role & 1 ? 5 : 0;                                  // the first of them
+  float kk[5][4], qk[5][4];
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
+  for (int j = 0; j < 5; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) kk[nt][i] = qk[nt][i] = 0.f;
-#pragma unroll 2
-  for (int kt = 0; kt < 8; ++kt) {
-    uint32_t fk[4], fq[4];
-    ldmatrix_x4(sk + swz(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fk);
-    ldmatrix_x4(sq + swz(mt * 16 + (mi & 1) * 8 + mr, kt * 2 + (mi >> 1)), fq);
+    for (int i = 0; i < 4; ++i) kk[j][i] = qk[j][i] = 0.f;
+#pragma unroll 1
+  for (int k2 = 0; k2 < 4; ++k2) {  // 32 columns of K and Q
+    uint32_t fb[5][4];
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      if (np <= mt) {
-        uint32_t fb[4];
-        ldmatrix_x4(sk + swz(np * 16 + (mi >> 1) * 8 + mr, kt * 2 + (mi & 1)), fb);
-        mma_bf16_16816(kk[np * 2], fk, fb[0], fb[1]);
-        mma_bf16_16816(kk[np * 2 + 1], fk, fb[2], fb[3]);
-        mma_bf16_16816(qk[np * 2], fq, fb[0], fb[1]);
-        mma_bf16_16816(qk[np * 2 + 1], fq, fb[2], fb[3]);
+    for (int j = 0; j < 5; ++j) {
+      const int nt = j < n_a ? nt0 + j : j - n_a;
+      ldmatrix_x4(sk + swz(nt * 8 + mr, k2 * 4 + mi), fb[j]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t fk[4], fq[4];
+      const int unit = k2 * 4 + e * 2 + (mi >> 1), r = (mi & 1) * 8 + mr;
+      ldmatrix_x4(sk + swz(mt_a * 16 + r, unit), fk);
+      ldmatrix_x4(sq + swz(mt_a * 16 + r, unit), fq);
+#pragma unroll
+      for (int j = 0; j < 5; ++j)
+        if (j < n_a) {
+          mma_bf16_16816(kk[j], fk, fb[j][2 * e], fb[j][2 * e + 1]);
+          mma_bf16_16816(qk[j], fq, fb[j][2 * e], fb[j][2 * e + 1]);
+        }
+      if (role & 1) {
+        ldmatrix_x4(sk + swz(mt_b * 16 + r, unit), fk);
+        ldmatrix_x4(sq + swz(mt_b * 16 + r, unit), fq);
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+          if (j >= n_a) {
+            mma_bf16_16816(kk[j], fk, fb[j][2 * e], fb[j][2 * e + 1]);
+            mma_bf16_16816(qk[j], fq, fb[j][2 * e], fb[j][2 * e + 1]);
+          }
       }
     }
   }
@@ -462,49 +477,39 @@ __global__ void __launch_bounds__(kPrepThreads, kGroup ? 4 : 5) delta_prep_kerne
     scal[128 + tid] = a.scale * eg * sm.inq[tid];
     if (tid == 0) scal[192] = expf(ge.x + ge.y);
   }
-  float2 gi[2];
-  float fa[2], fp[2];
-  int row[2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int i = mt * 16 + (lane >> 2) + half * 8;
-    row[half] = i;
-    gi[half] = sm.G[i];
-    fa[half] = sm.beta[i] * sm.ink[i];
-    fp[half] = a.scale * sm.inq[i];
-  }
+  for (int t = 0; t < 5; ++t) {
+    const int mt = t < n_a ? mt_a : mt_b, nt = t < n_a ? nt0 + t : t - n_a;
+    const int j = nt * 8 + (lane & 3) * 2;
+    const float4 gj = *reinterpret_cast<const float4*>(sm.G + j);
+    const float2 ik = *reinterpret_cast<const float2*>(sm.ink + j);
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt) {
-    if (nt < 2 * (mt + 1)) {
-      const int j = nt * 8 + (lane & 3) * 2;
-      const float4 gj = *reinterpret_cast<const float4*>(sm.G + j);
-      const float2 ik = *reinterpret_cast<const float2*>(sm.ink + j);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = row[half];
-        // e^(G_i - G_j): the high parts cancel exactly where it matters
-        const float d0 = j <= i ? __expf((gi[half].x - gj.x) + (gi[half].y - gj.y)) * ik.x : 0.f;
-        const float d1 = j < i ? __expf((gi[half].x - gj.z) + (gi[half].y - gj.w)) * ik.y : 0.f;
-        float2 x;
-        x.x = j < i ? fa[half] * d0 * kk[nt][half * 2] : 0.f;
-        x.y = j + 1 < i ? fa[half] * d1 * kk[nt][half * 2 + 1] : 0.f;
-        *reinterpret_cast<float2*>(sm.A + i * kPrepLd + j) = x;
-        *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + tri_unit(i, nt) + (lane & 3) * 4) =
-            pack_bf16x2(j <= i ? fp[half] * d0 * qk[nt][half * 2] : 0.f,
-                        j < i ? fp[half] * d1 * qk[nt][half * 2 + 1] : 0.f);
-      }
-    } else if (nt < 2 * ((mt | 1) + 1)) {  // above the diagonal inside a 32 x 32 block
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        *reinterpret_cast<float2*>(sm.A + row[half] * kPrepLd + nt * 8 + (lane & 3) * 2) =
-            make_float2(0.f, 0.f);
+    for (int half = 0; half < 2; ++half) {
+      const int i = mt * 16 + (lane >> 2) + half * 8;
+      const float2 gi = sm.G[i];
+      const float fa = sm.beta[i] * sm.ink[i], fp = a.scale * sm.inq[i];
+      // e^(G_i - G_j): the high parts cancel exactly where it matters
+      const float d0 = j <= i ? __expf((gi.x - gj.x) + (gi.y - gj.y)) * ik.x : 0.f;
+      const float d1 = j < i ? __expf((gi.x - gj.z) + (gi.y - gj.w)) * ik.y : 0.f;
+      float2 x;
+      x.x = j < i ? fa * d0 * kk[t][half * 2] : 0.f;
+      x.y = j + 1 < i ? fa * d1 * kk[t][half * 2 + 1] : 0.f;
+      *reinterpret_cast<float2*>(sm.A + i * kPrepLd + j) = x;
+      *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + tri_unit(i, nt) + (lane & 3) * 4) =
+          pack_bf16x2(j <= i ? fp * d0 * qk[t][half * 2] : 0.f,
+                      j < i ? fp * d1 * qk[t][half * 2 + 1] : 0.f);
     }
   }
-  __syncwarp();  // a warp's own rows hold its diagonal block
+  if (tid < 64) {  // above the diagonal inside the 32 x 32 blocks
+    const int i = (tid >> 5) * 32 + (tid & 31) / 2, j = (tid >> 5) * 32 + 16 + (tid & 1) * 8;
+    *reinterpret_cast<float4*>(sm.A + i * kPrepLd + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(sm.A + i * kPrepLd + j + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
   {
     // column c of the block's inverse: x_i = [i == c] - sum_{m < i} A_im x_m
     const int c = lane & 15;
-    float* A = sm.A + mt * 16 * kPrepLd + mt * 16;
+    float* A = sm.A + warp * 16 * (kPrepLd + 1);
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = 0.f;
@@ -536,32 +541,41 @@ __global__ void __launch_bounds__(kPrepThreads, kGroup ? 4 : 5) delta_prep_kerne
   {  // pair `part` of 16 x 16 blocks; rows 8 half .. of the block below
     float* T1 = sm.A + part * 32 * (kPrepLd + 1);
     float* A21 = T1 + 16 * kPrepLd;
-    float y[2][4] = {}, t[4] = {};
-    prep_product<2>(T1, A21, 0, 1, 2, y);
-    uint32_t fy[3][4], fb[3][2];
-    split_frag<3>(y[0], y[1], fy);
-    prep_right(A21 + 16 + half * 8 * kPrepLd, fb);
-    prep_mma(t, fy, fb);
+    float y[2][4] = {}, t[1][4] = {};
+    uint32_t fx[3][4], fb[2][3][2], f2[1][3][2];
+    prep_left(T1, fx);
+    prep_right(A21, fb[0]);
+    prep_right(A21 + 8 * kPrepLd, fb[1]);
+    prep_right(A21 + 16 + half * 8 * kPrepLd, f2[0]);
+    prep_mma(y, fx, fb);
+    split_frag<3>(y[0], y[1], fx);
+    prep_mma(t, fx, f2);
     __syncthreads();
-    prep_store(A21 + half * 8 * kPrepLd, t);
+    prep_store(A21 + half * 8 * kPrepLd, t[0]);
   }
   __syncthreads();
   {  // columns 16 part .. of the 32 x 32 block below, rows 16 half ..
     float* A21 = sm.A + 32 * kPrepLd;
     float y[4][4] = {}, t[2][4] = {};
+    uint32_t fx[3][4];
     // T1 and T2 are lower triangular: rows 16 part .. of T1, and the first 16 (half + 1) of Y
-    prep_product<4>(sm.A + part * 16, A21, part, 2, 2 * (half + 1), y);
+#pragma unroll 1
+    for (int kt = part; kt < 2; ++kt) {
+      uint32_t fb[4][3][2];
+      prep_left(sm.A + kt * 16 * kPrepLd + part * 16, fx);
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) prep_right(A21 + nt * 8 * kPrepLd + kt * 16, fb[nt]);
+      prep_mma(y, fx, fb);
+    }
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
       if (kt > half) continue;
-      uint32_t fy[3][4];
-      split_frag<3>(y[2 * kt], y[2 * kt + 1], fy);
+      uint32_t fb[2][3][2];
+      split_frag<3>(y[2 * kt], y[2 * kt + 1], fx);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t fb[3][2];
-        prep_right(A21 + 32 + (half * 16 + e * 8) * kPrepLd + kt * 16, fb);
-        prep_mma(t[e], fy, fb);
-      }
+      for (int e = 0; e < 2; ++e)
+        prep_right(A21 + 32 + (half * 16 + e * 8) * kPrepLd + kt * 16, fb[e]);
+      prep_mma(t, fx, fb);
     }
     __syncthreads();
 #pragma unroll
@@ -569,22 +583,23 @@ __global__ void __launch_bounds__(kPrepThreads, kGroup ? 4 : 5) delta_prep_kerne
   }
   __syncthreads();
   // T diag(beta) in three pieces, eight columns at a time
-#pragma unroll
-  for (int n = 0; n < kDeltaChunk * 8 / kPrepThreads; ++n) {
-    const int at = tid + n * kPrepThreads, i = at >> 3, c = at & 7;
-    if (c >= 2 * ((i >> 4) + 1)) continue;
+#pragma unroll 1
+  for (int at = tid; at < kDeltaMat / 16; at += kPrepThreads) {
+    const int block = at >> 5, m = block >= 6 ? 3 : block >= 3 ? 2 : block >= 1 ? 1 : 0;
+    const int r = (at & 31) >> 1, unit = (at & 1) ^ ((r >> 2) & 1);
+    const int i = m * 16 + r, c = (block - ((m * (m + 1)) >> 1)) * 16 + unit * 8;
     uint32_t p[4][3];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float4 t = *reinterpret_cast<const float4*>(sm.A + i * kPrepLd + c * 8 + e * 4);
-      const float4 w = *reinterpret_cast<const float4*>(sm.beta + c * 8 + e * 4);
+      const float4 t = *reinterpret_cast<const float4*>(sm.A + i * kPrepLd + c + e * 4);
+      const float4 w = *reinterpret_cast<const float4*>(sm.beta + c + e * 4);
       split_pair<3>(t.x * w.x, t.y * w.y, p[2 * e]);
       split_pair<3>(t.z * w.z, t.w * w.w, p[2 * e + 1]);
     }
 #pragma unroll
-    for (int m = 0; m < 3; ++m)
-      *reinterpret_cast<uint4*>(dst + m * kDeltaMat + tri_unit(i, c)) =
-          make_uint4(p[0][m], p[1][m], p[2][m], p[3][m]);
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<uint4*>(dst + k * kDeltaMat + at * 16) =
+          make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
   }
   if (kGroup && hl + 1 < hl0 + per) {
     __syncthreads();
