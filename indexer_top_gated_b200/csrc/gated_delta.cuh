@@ -633,9 +633,9 @@ constexpr int kScanV = 2 * kDeltaTile;
 constexpr int kScanItem = kScanV + kDeltaChunk * kScanNV * 2;
 constexpr int kScanBytes = kScanItem + kDeltaItemBytes;
 constexpr int kScanStage = (kScanBytes + 1023) / 1024 * 1024;
-// exchange areas of 16 value columns, 512 bytes (a fragment of a warp) each unit: S [8 key tiles]
-// [2 pieces], R [2 warps][4], X [4 token tiles][3 pieces], U and U' [4 token tiles][2 + 3]
-constexpr int kExS = 0, kExR = kExS + 16 * 512, kExX = kExR + 8 * 512, kExU = kExX + 12 * 512;
+// exchange areas of 16 value columns, 512 bytes (a fragment of a warp) each unit: S [2 chunks][8
+// key tiles][2 pieces], R [2 warps][4], X [4 token tiles][3 pieces], U and U' [4 token tiles][2 + 3]
+constexpr int kExS = 0, kExR = kExS + 2 * 16 * 512, kExX = kExR + 8 * 512, kExU = kExX + 12 * 512;
 constexpr int kScanExch = kExU + 20 * 512;
 constexpr int kScanBars = 2 * kScanStage + kScanPairs * kScanExch;
 constexpr int kScanSmem = kScanBars + 64;
@@ -649,6 +649,10 @@ struct ScanSync {
 
 // 16-byte unit u (value columns 8u .. 8u+7) of token r in the V tile, rows of 64 bytes
 DSA_DEV uint32_t swz64(int r, int u) { return r * 64 + ((u ^ ((r >> 1) & 3)) << 4); }
+
+DSA_DEV void named_barrier_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 
 DSA_DEV void st_frag(unsigned char* p, const uint32_t (&f)[4]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(f[0], f[1], f[2], f[3]);
@@ -713,7 +717,6 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
   const int bar = 1 + 3 * pair;
   const int tile[2] = {tri_tile(w, 0), tri_tile(w, 1)};
   const int their[2] = {tri_tile(1 - w, 0), tri_tile(1 - w, 1)};
-  const int kt4 = w ? 1 : 3;
   ex += lane * 16;
 
   // S^T of this warp: rows dv0 + lane/4 (+8), columns 64 w + 8 n + 2 (lane % 4) (+1)
@@ -764,11 +767,14 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
     };
     load_k(0, fb[0]);
     uint32_t fs[4][2][4];
+    // (the output warps may still read the last chunk's S, in the other of two areas; they are
+    // done with the one before that once bar + 1 is passed)
+    unsigned char* ex_s = ex + kExS + (c & 1) * 16 * 512;
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
       split_frag<2>(s[2 * kt], s[2 * kt + 1], fs[kt]);
-      st_frag(ex + kExS + ((w * 4 + kt) * 2) * 512, fs[kt][0]);
-      st_frag(ex + kExS + ((w * 4 + kt) * 2 + 1) * 512, fs[kt][1]);
+      st_frag(ex_s + ((w * 4 + kt) * 2) * 512, fs[kt][0]);
+      st_frag(ex_s + ((w * 4 + kt) * 2 + 1) * 512, fs[kt][1]);
     }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
@@ -787,7 +793,7 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
     for (int n = 0; n < 4; ++n)
       *reinterpret_cast<float4*>(ex + kExR + (w * 4 + n) * 512) =
           make_float4(r[4 + n][0], r[4 + n][1], r[4 + n][2], r[4 + n][3]);
-    uint32_t fv[2][4], ft[5][3][4];
+    uint32_t fv[2][4];
     float2 av[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -800,7 +806,8 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
     // so that their products take the tensor pipe while these exchange and round.  And the output
     // warps are done with the last chunk's U.
     named_barrier(bar + 1, 128);
-    // X^T = V^T - R^T diag(a) of the own tokens, handed to both warps in three pieces
+    // X^T = V^T - R^T diag(a) of the own tokens, in three pieces, and to the other warp
+    uint32_t fx[2][3][4], ft[3][3][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x[2][4];
@@ -814,22 +821,21 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
         x[e][2] = bf16_lo(fv[i][2 * e + 1]) - av[i][e].x * (own[2] + o.z);
         x[e][3] = bf16_hi(fv[i][2 * e + 1]) - av[i][e].y * (own[3] + o.w);
       }
-      uint32_t f[3][4];
-      split_frag<3>(x[0], x[1], f);
+      split_frag<3>(x[0], x[1], fx[i]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) st_frag(ex + kExX + (tile[i] * 3 + p) * 512, f[p]);
+      for (int p = 0; p < 3; ++p) st_frag(ex + kExX + (tile[i] * 3 + p) * 512, fx[i][p]);
     }
+    auto load_t = [&](int own, int kt, uint32_t (&f)[3][4]) {
 #pragma unroll
-    for (int b = 0; b < 5; ++b) {
-      const uint32_t row = b < 4 ? t_row[tri_own(b)] + tri_kt(b) * 512
-                                 : (w ? t_row[0] : t_row[1]) + kt4 * 512;
-#pragma unroll
-      for (int p = 0; p < 3; ++p) ldmatrix_x4(st + p * kDeltaMat + row, ft[b][p]);
-    }
-    named_barrier(bar, 64);
+      for (int p = 0; p < 3; ++p) ldmatrix_x4(st + p * kDeltaMat + t_row[own] + kt * 512, f[p]);
+    };
+    load_t(0, tile[0], ft[0]);
+    load_t(1, tile[0], ft[1]);
+    load_t(1, tile[1], ft[2]);
 
     // U^T = X^T T^T of the own tokens; products of pieces below 2^-24 of the whole are left out.
-    // Accumulators: first tile; second tile, even and odd blocks; block 4
+    // First the blocks over the own tokens' X, under the exchange: (first tile, first), (second,
+    // first), (second, second).
     float u[4][2][4];
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -838,22 +844,34 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[n][e][i] = 0.f;
 #pragma unroll
-    for (int px = 0; px < 3; ++px) {
-      uint32_t fx[4][4];
-#pragma unroll
-      for (int kt = 0; kt < 3; ++kt) ld_frag(ex + kExX + (kt * 3 + px) * 512, fx[kt]);
-      ld_frag(ex + kExX + (kt4 * 3 + px) * 512, fx[3]);
+    for (int px = 0; px < 3; ++px)
 #pragma unroll
       for (int pt = 0; pt < 3 - px; ++pt)
 #pragma unroll
-        for (int b = 0; b < 5; ++b) {
-          float(&acc)[2][4] = u[b == 1 ? 0 : b == 4 ? 3 : b == 2 ? 2 : 1];
-          const uint32_t(&x)[4] = fx[b < 4 ? tri_kt(b) : 3];
-          mma_bf16_16816(acc[0], x, ft[b][pt][0], ft[b][pt][1]);
-          mma_bf16_16816(acc[1], x, ft[b][pt][2], ft[b][pt][3]);
-        }
+        for (int b = 0; b < 3; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            mma_bf16_16816(u[b][e], fx[b >> 1][px], ft[b][pt][2 * e], ft[b][pt][2 * e + 1]);
+    // Then those over the other's: tiles 1 and 2 in tile 3, or tile 0 in tiles 1 and 2
+    load_t(w ? 0 : 1, their[0], ft[0]);
+    load_t(1, w ? their[0] : their[1], ft[1]);
+    named_barrier(bar, 64);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      ld_frag(ex + kExX + (their[0] * 3 + p) * 512, fx[0][p]);
+      ld_frag(ex + kExX + ((w ? their[0] : their[1]) * 3 + p) * 512, fx[1][p]);
     }
-    // U to the output warps, U' = U diag(t) in three pieces for S
+#pragma unroll
+    for (int px = 0; px < 3; ++px)
+#pragma unroll
+      for (int pt = 0; pt < 3 - px; ++pt)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            mma_bf16_16816(u[b ? 1 : 3][e], fx[b][px], ft[b][pt][2 * e], ft[b][pt][2 * e + 1]);
+    // U to the output warps; U' = U diag(t) in three pieces for S, and to the other warp
+    uint32_t fu[2][3][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x[2][4], y[2][4];
@@ -871,57 +889,48 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
         y[e][2] = x[e][2] * tv.x;
         y[e][3] = x[e][3] * tv.y;
       }
-      uint32_t f3[3][4];
-      split_frag<3>(y[0], y[1], f3);
+      split_frag<3>(y[0], y[1], fu[i]);
       unsigned char* to = ex + kExU + tile[i] * 5 * 512;
 #pragma unroll
-      for (int p = 0; p < 3; ++p) st_frag(to + (2 + p) * 512, f3[p]);
+      for (int p = 0; p < 3; ++p) st_frag(to + (2 + p) * 512, fu[i][p]);
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         *reinterpret_cast<float4*>(to + e * 512) = make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
     }
+    named_barrier_arrive(bar + 2, 128);  // the output warps may read U
     // S = e^(G_C) S + U'^T K over this warp's key columns
-    // (32 at a time, so that the first half is rounded for the next chunk under the second)
-    auto load_kt = [&](int half, int kt, uint32_t (&f)[4]) {
-      ldmatrix_x4_trans(sk + swz(kt * 16 + (mi & 1) * 8 + mr, w * 8 + half * 2 + (mi >> 1)), f);
-    };
+    // over the own tokens under the exchange of U', then the other's
+    auto load_kt = [&](int t, uint32_t (&f)[4][4]) {
 #pragma unroll
-    for (int np = 0; np < 2; ++np) {
-      load_kt(np, 0, fb[0][np]);
-      load_kt(np, 1, fb[0][2 + np]);
-    }
+      for (int np = 0; np < 4; ++np)
+        ldmatrix_x4_trans(
+            sk + swz(t * 16 + (mi & 1) * 8 + mr, w * 8 + np * 2 + (mi >> 1)), f[np]);
+    };
+    load_kt(tile[0], fb[0]);
     const float decay = scal[192];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[n][i] *= decay;
-    named_barrier(bar + 2, 128);
-    uint32_t fu[4][3][4];
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt)
+    for (int g = 0; g < 4; ++g) {
+      if (g < 3) load_kt(g == 0 ? tile[1] : their[g - 1], fb[(g + 1) & 1]);
+      if (g == 2) {
+        named_barrier(bar, 64);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) ld_frag(ex + kExU + (kt * 5 + 2 + p) * 512, fu[kt][p]);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {  // half g >> 1 of the columns, token tiles 2 (g & 1) and the next
-      if (g < 3) {
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-          load_kt(((g + 1) >> 1) * 2 + np, 2 * ((g + 1) & 1), fb[(g + 1) & 1][np]);
-          load_kt(((g + 1) >> 1) * 2 + np, 2 * ((g + 1) & 1) + 1, fb[(g + 1) & 1][2 + np]);
-        }
+          for (int p = 0; p < 3; ++p)
+            ld_frag(ex + kExU + (their[i] * 5 + 2 + p) * 512, fu[i][p]);
       }
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
+      for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-#pragma unroll
-          for (int np = 0; np < 2; ++np) {
-            const uint32_t(&f)[4] = fb[g & 1][kt * 2 + np];
-            const uint32_t(&x)[4] = fu[2 * (g & 1) + kt][p];
-            const int n = (g >> 1) * 4 + np * 2;
-            mma_bf16_16816(s[n], x, f[0], f[1]);
-            mma_bf16_16816(s[n + 1], x, f[2], f[3]);
-          }
+        for (int np = 0; np < 4; ++np) {
+          const uint32_t(&f)[4] = fb[g & 1][np];
+          mma_bf16_16816(s[2 * np], fu[g & 1][p], f[0], f[1]);
+          mma_bf16_16816(s[2 * np + 1], fu[g & 1][p], f[2], f[3]);
+        }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sy->empty[c & 1]));
@@ -971,7 +980,7 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
     };
     auto load_s = [&](int kt, uint32_t (&f)[2][4]) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) ld_frag(ex + kExS + (kt * 2 + p) * 512, f[p]);
+      for (int p = 0; p < 2; ++p) ld_frag(ex + kExS + (c & 1) * 16 * 512 + (kt * 2 + p) * 512, f[p]);
     };
     load_q(0, fq[0]);
     named_barrier(bar + 1, 128);
