@@ -446,25 +446,38 @@ def _rows(where, name, t, dtype, shape, device):
     return t.data_ptr(), steps[0]
 
 
+def _torch():
+    """torch, imported on first use (loading the library does not need it)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
+
+
 def _device(stream) -> int:
-    device = _cuda().current_device()
+    device = _torch().cuda.current_device()
     if stream is not None and stream.device.index != device:
         _bad("stream", f"of {stream.device} while cuda:{device} is current")
     return device
 
 
-def _cuda():
-    import torch
-    return torch.cuda
-
-
 def _raw_stream(stream, device) -> int:
-    return _cuda().current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+    """Handle of `stream`, or of the device's current one (without building a Stream object)."""
+    return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _output(where, name, t, dtype, shape, device) -> int:
+    if t is None:
+        _bad(where, f"an input without its {name}")
+    return _tensor(where, name, t, dtype, shape, device)
 
 
 def _index(where, name, t, n, device):
-    import torch
-    return None if t is None else _tensor(where, name, t, torch.int32, (n,), device)
+    return None if t is None else _tensor(where, name, t, _torch().int32, (n,), device)
 
 
 def dsa_rope_append(shape: LayerShape, rg: Ragged, rope: RopeShape, q=None, k=None, v=None,
@@ -472,32 +485,30 @@ def dsa_rope_append(shape: LayerShape, rg: Ragged, rope: RopeShape, q=None, k=No
                     q_idx_out=None, k_idx_cache=None, positions=None, err_count=None, stream=None):
     """Rotary positions of the batch's new rows: q and q_idx to q_out and q_idx_out, k, v and
     k_idx to the cache rows of their positions.  Inputs left out leave their outputs out."""
-    import torch
-    where, device = "dsa_rope_append", _device(stream)
+    where, device, torch = "dsa_rope_append", _device(stream), _torch()
     bf16 = torch.bfloat16
     idx_type = torch.float8_e4m3fn if shape.idx_dtype == DSA_FP8_E4M3 else bf16
     o, b = rope.params(), RopeBuffers()
     n, rows, d, di = rg.total_q, rg.total_kv, shape.head_dim, shape.idx_dim
 
-    def put(name, t, to_name, to, heads, dim, to_rows, to_type):
-        if to is None:
-            _bad(where, f"{name} without {to_name}")
-        at, step = _rows(where, name, t, bf16, (n, heads, dim), device)
-        setattr(b, name, at)
-        if step:
-            setattr(o, name + "_row_stride", step)
-        setattr(b, to_name, _tensor(where, to_name, to, to_type, (to_rows, heads, dim), device))
-
     if q is not None:
-        put("q", q, "q_out", q_out, shape.n_q_heads, d, n, bf16)
+        shp = (n, shape.n_q_heads, d)
+        b.q, o.q_row_stride = _rows(where, "q", q, bf16, shp, device)
+        b.q_out = _output(where, "q_out", q_out, bf16, shp, device)
     if k is not None:
-        put("k", k, "k_cache", k_cache, shape.n_kv_heads, d, rows, bf16)
+        b.k, o.k_row_stride = _rows(where, "k", k, bf16, (n, shape.n_kv_heads, d), device)
+        b.k_cache = _output(where, "k_cache", k_cache, bf16, (rows, shape.n_kv_heads, d), device)
     if v is not None:
-        put("v", v, "v_cache", v_cache, shape.n_kv_heads, d, rows, bf16)
+        b.v, o.v_row_stride = _rows(where, "v", v, bf16, (n, shape.n_kv_heads, d), device)
+        b.v_cache = _output(where, "v_cache", v_cache, bf16, (rows, shape.n_kv_heads, d), device)
     if q_idx is not None:
-        put("q_idx", q_idx, "q_idx_out", q_idx_out, shape.n_idx_heads, di, n, idx_type)
+        shp = (n, shape.n_idx_heads, di)
+        b.q_idx, o.q_idx_row_stride = _rows(where, "q_idx", q_idx, bf16, shp, device)
+        b.q_idx_out = _output(where, "q_idx_out", q_idx_out, idx_type, shp, device)
     if k_idx is not None:
-        put("k_idx", k_idx, "k_idx_cache", k_idx_cache, shape.n_idx_heads, di, rows, idx_type)
+        ni = shape.n_idx_heads
+        b.k_idx, o.k_idx_row_stride = _rows(where, "k_idx", k_idx, bf16, (n, ni, di), device)
+        b.k_idx_cache = _output(where, "k_idx_cache", k_idx_cache, idx_type, (rows, ni, di), device)
     rc = lib.dsa_rope_append(ctypes.byref(shape.params()), ctypes.byref(rg), ctypes.byref(o),
                              ctypes.byref(b), _index(where, "positions", positions, n, device),
                              _index(where, "err_count", err_count, 1, device),
@@ -509,9 +520,8 @@ def dsa_short_conv(conv: ConvShape, rg: Ragged, x, weight, out, bias=None, state
                    state_out=None, state_index=None, stream=None):
     """Short causal convolution of x [total_q, channels] into out, rows before a sequence's
     first from state_in [slots, width - 1, channels], the last ones to state_out."""
-    import torch
     where, device = "dsa_short_conv", _device(stream)
-    bf16, c = torch.bfloat16, conv.channels
+    bf16, c = _torch().bfloat16, conv.channels
     px, sx = _rows(where, "x", x, bf16, (rg.total_q, c), device)
     po, so = _rows(where, "out", out, bf16, (rg.total_q, c), device)
     pw = _tensor(where, "weight", weight, bf16, (c, conv.width), device)
@@ -538,8 +548,7 @@ def _delta_params(delta: DeltaShape, n_states: int = 0, strides=(0, 0, 0)) -> De
 
 
 def _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out, state_index, device):
-    import torch
-    bf16, f32 = torch.bfloat16, torch.float32
+    bf16, f32 = _torch().bfloat16, _torch().float32
     n, hv, d = rg.total_q, delta.n_v_heads, delta.head_dim
     qk, vo, gb = (n, delta.n_k_heads, d), (n, hv, d), (n, hv)
     pq, sq = _rows(where, "q", q, bf16, qk, device)
