@@ -545,7 +545,8 @@ typedef struct {
  *   workspace   device, 256-byte aligned, ws_bytes >= the minimum of
  *               dsa_gated_delta_workspace_size (one head's chunks; the heads run in as many
  *               passes as that needs, the recommended size holds all).  0 bytes, and NULL, when
- *               max_q_len <= 16.
+ *               max_q_len <= 16.  Calls that can overlap on the GPU (other streams, captured
+ *               graphs that replay at once) need a workspace each.
  * Only batch, q_offsets, max_q_len, total_q and q_offsets_host of dsa_ragged are read.
  * Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps no input and
  * no state; state_out is state_in or does not overlap it.

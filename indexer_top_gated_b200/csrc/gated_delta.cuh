@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
 
 // ------------------------------------------------------------------ chunked form: the scan
 //
-// A CTA walks one sequence's chunks for one head and kScanNV of its 128 value columns.  Products
+// A CTA walks one sequence's chunks for one head and 32 (or 16) of its 128 value columns.  Products
 // are taken transposed, with 16 value columns as the rows of the tensor-core tile:
 //   R^T = S K^T, QS^T = S Q^T, U^T = X^T T^T, S += U'^T K, O^T = QS^T + U^T P^T
 // so that an accumulator tile is, register for register, the next product's left operand, and
@@ -624,10 +624,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
 // one another in four stages); the tensor pipe, which the output warps fill in the gaps, is the
 // next limit (304 a scheduler and chunk).  So accumulators alternate, eight or six between two
 // uses of one, and operands are fetched one step ahead.
-constexpr int kScanNV = 32;
-constexpr int kScanPairs = kScanNV / 16;
-constexpr int kScanWorkers = kScanPairs * 4;  // warps
-constexpr int kScanThreads = kScanWorkers * 32 + 32;
+constexpr int kScanNV = 32;  // value columns of a V tile
 // one chunk's operands: K, Q, V, the workspace item
 constexpr int kScanV = 2 * kDeltaTile;
 constexpr int kScanItem = kScanV + kDeltaChunk * kScanNV * 2;
@@ -637,8 +634,16 @@ constexpr int kScanStage = (kScanBytes + 1023) / 1024 * 1024;
 // key tiles][2 pieces], R [2 warps][4], X [4 token tiles][3 pieces], U and U' [4 token tiles][2 + 3]
 constexpr int kExS = 0, kExR = kExS + 2 * 16 * 512, kExX = kExR + 8 * 512, kExU = kExX + 12 * 512;
 constexpr int kScanExch = kExU + 20 * 512;
-constexpr int kScanBars = 2 * kScanStage + kScanPairs * kScanExch;
-constexpr int kScanSmem = kScanBars + 64;
+// PAIRS sets of four warps (16 value columns each) in a CTA: 2, or 1 where there are too few
+// (sequence, head)s to fill the GPU with 2
+template <int PAIRS>
+struct ScanGeo {
+  static constexpr int kParts = kDeltaDim / (16 * PAIRS);  // CTAs of a (sequence, head)
+  static constexpr int kWorkers = PAIRS * 4;               // warps
+  static constexpr int kThreads = kWorkers * 32 + 32;
+  static constexpr int kBars = 2 * kScanStage + PAIRS * kScanExch;
+  static constexpr int kSmem = kBars + 64;
+};
 
 // Barriers of the two stages: full (the loader's bytes), empty (the worker warps); of the last
 // chunk's rows; and the flag that a wait has given up.
@@ -1063,14 +1068,15 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
   }
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(
+template <int PAIRS>
+__global__ void __launch_bounds__(ScanGeo<PAIRS>::kThreads, 1) delta_scan_kernel(
     const DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
+  using Geo = ScanGeo<PAIRS>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5;
-  constexpr int kParts = kDeltaDim / kScanNV;
-  const int part = blockIdx.x % kParts;
-  const int hl = (blockIdx.x / kParts) % a.heads;
-  const int b = blockIdx.x / (kParts * a.heads);
+  const int part = blockIdx.x % Geo::kParts;
+  const int hl = (blockIdx.x / Geo::kParts) % a.heads;
+  const int b = blockIdx.x / (Geo::kParts * a.heads);
   ScanPlace at;
   at.h = a.head0 + hl;
   at.hk = at.h / (a.hv / a.hk);
@@ -1078,25 +1084,26 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(
   at.len = (int)(__ldg(a.q_offsets + b + 1) - at.first);
   if (at.len < a.min_len) return;
   at.slot = delta_slot(a, b);
-  at.dvc = part * kScanNV;
+  at.dvc = part * PAIRS / 2 * kScanNV;
   at.items = a.ws + (delta_first_slot(a, b) * a.heads + hl) * (int64_t)kDeltaItemBytes;
   at.item_step = (int64_t)a.heads * kDeltaItemBytes;
-  ScanSync* sy = reinterpret_cast<ScanSync*>(smem + kScanBars);
+  ScanSync* sy = reinterpret_cast<ScanSync*>(smem + Geo::kBars);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sy->full[i]), 1);
-      mbar_init(smem_u32(&sy->empty[i]), kScanWorkers);
+      mbar_init(smem_u32(&sy->empty[i]), Geo::kWorkers);
     }
     mbar_init(smem_u32(&sy->tail), 1);
     sy->abort = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  // chain warps, then output warps (one of each on every scheduler), then the loader
-  const int pair = (warp >> 1) % kScanPairs;
-  unsigned char* ex = smem + 2 * kScanStage + pair * kScanExch;
-  if (warp == kScanWorkers) scan_loader(a, maps, at, smem, sy);
-  else if (warp < 2 * kScanPairs) scan_chain(a, at, smem, sy, ex, pair, warp & 1);
+  // chain warps, then output warps (spread over the schedulers), then the loader.  `pair`: which
+  // half of the V tile
+  const int set = (warp >> 1) % PAIRS, pair = PAIRS == 1 ? part & 1 : set;
+  unsigned char* ex = smem + 2 * kScanStage + set * kScanExch;
+  if (warp == Geo::kWorkers) scan_loader(a, maps, at, smem, sy);
+  else if (warp < 2 * PAIRS) scan_chain(a, at, smem, sy, ex, pair, warp & 1);
   else scan_output(a, at, smem, sy, ex, pair, warp & 1);
 }
 

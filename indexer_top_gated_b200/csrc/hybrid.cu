@@ -99,7 +99,8 @@ cudaError_t hybrid_allow_smem() {
   };
   cudaError_t e = allow((const void*)delta_prep_kernel<false>, (int)sizeof(PrepSmem));
   e = e ? e : allow((const void*)delta_prep_kernel<true>, (int)sizeof(PrepSmem));
-  e = e ? e : allow((const void*)delta_scan_kernel, kScanSmem);
+  e = e ? e : allow((const void*)delta_scan_kernel<1>, ScanGeo<1>::kSmem);
+  e = e ? e : allow((const void*)delta_scan_kernel<2>, ScanGeo<2>::kSmem);
   return e;
 }
 
@@ -366,10 +367,12 @@ dsa_status launch_recurrent(DeltaArgs a, int max_len, cudaStream_t st) {
   return launched("delta_recurrent_kernel");
 }
 
+template <int PAIRS>
 dsa_status launch_scan(const DeltaArgs& a, const DeltaMaps& maps, cudaStream_t st) {
-  const int64_t ctas = (int64_t)a.batch * a.heads * (kDeltaDim / kScanNV);
+  using Geo = ScanGeo<PAIRS>;
+  const int64_t ctas = (int64_t)a.batch * a.heads * Geo::kParts;
   if (ctas > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  delta_scan_kernel<<<(unsigned)ctas, kScanThreads, kScanSmem, st>>>(a, maps);
+  delta_scan_kernel<PAIRS><<<(unsigned)ctas, Geo::kThreads, Geo::kSmem, st>>>(a, maps);
   return launched("delta_scan_kernel");
 }
 
@@ -440,7 +443,12 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
     else
       delta_prep_kernel<false><<<ctas, kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
     DSA_TRY(launched("delta_prep_kernel"));
-    DSA_TRY(launch_scan(a, maps, st));
+    // 16 value columns a CTA while those CTAs fit the GPU at once: a pair of chain warps alone on
+    // an SM is faster (XXX)
+    if ((int64_t)a.batch * a.heads * ScanGeo<1>::kParts <= dev.num_sms)
+      DSA_TRY(launch_scan<1>(a, maps, st));
+    else
+      DSA_TRY(launch_scan<2>(a, maps, st));
   }
   return DSA_OK;
 }

@@ -460,6 +460,35 @@ def test_delta_many_heads_take_wide_parts():
     assert torch.equal(o, out) and torch.equal(s, st)
 
 
+@pytest.mark.parametrize("lens", [[70, 65], [65, 3, 70]])
+def test_delta_sequences_do_not_touch_one_another(lens):
+    """NaN and infinities in one sequence leave the others, whose last chunks end beside it, alone."""
+    d = _Delta(lens, 1, 2)
+    want = d.call()
+    a, b = lens[0], lens[0] + lens[1]
+    for x, bad in ((d.q, math.nan), (d.k, math.inf), (d.v, math.nan), (d.g, math.nan), (d.beta, math.inf)):
+        x[a:b] = bad
+    out, st = d.call()
+    keep = torch.ones(sum(lens), dtype=torch.bool)
+    keep[a:b] = False
+    assert torch.equal(out[keep.cuda()], want[0][keep.cuda()])
+    for i, slot in enumerate(d.index.tolist()):
+        if i != 1:
+            assert torch.equal(st[slot], want[1][slot])
+
+
+def test_delta_scale_and_few_heads_of_many():
+    """An explicit scale; sequences times heads on both sides of the narrow parts' limit."""
+    for lens, hv in (([200, 90], 2), ([200, 90, 70, 100, 65], 6)):
+        d = _Delta(lens, 1, hv)
+        d.shape = dsa.DeltaShape(1, hv, scale=1 / math.sqrt(128))
+        out, st = d.call()
+        d.check(out, st)
+        d.shape = dsa.DeltaShape(1, hv)
+        again, st2 = d.call()
+        assert torch.equal(again, out) and torch.equal(st2, st)
+
+
 def test_delta_no_state_no_index_and_padding():
     d = _Delta([90, 1, 20], extra_rows=70)
     out, st = d.call(state_in=None)
