@@ -536,7 +536,7 @@ typedef struct {
  *   state_out   the same or NULL (not kept): the state after the sequence's last token (that
  *               before it, for a sequence without tokens).  May be state_in.
  *   state_index int32 [batch] or NULL, as for dsa_short_conv.
- * dsa_gated_delta_prefill takes any Q_b: sequences of up to 16 tokens run token by token, longer
+ * dsa_gated_delta_prefill takes any Q_b: sequences of up to 24 tokens run token by token, longer
  * ones in chunks of 64 (the state stays fp32; operands of the tensor-core products enter in
  * bf16 pieces that keep the state within about 1e-6 of itself).  A sequence's results depend
  * neither on the rest of the batch nor on the workspace's size.
@@ -545,7 +545,7 @@ typedef struct {
  *   workspace   device, 256-byte aligned, ws_bytes >= the minimum of
  *               dsa_gated_delta_workspace_size (one head's chunks; the heads run in as many
  *               passes as that needs, the recommended size holds all).  0 bytes, and NULL, when
- *               max_q_len <= 16.  Calls that can overlap on the GPU (other streams, captured
+ *               max_q_len <= 24.  Calls that can overlap on the GPU (other streams, captured
  *               graphs that replay at once) need a workspace each.
  * Only batch, q_offsets, max_q_len, total_q and q_offsets_host of dsa_ragged are read.
  * Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps no input and

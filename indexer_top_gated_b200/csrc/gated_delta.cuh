@@ -95,6 +95,26 @@ __global__ void __launch_bounds__(kRecWarps * 32) delta_recurrent_kernel(const D
   const int dv0 = (part * kRecWarps + warp) * kRecRows;
   const int64_t soff = ((slot * a.hv + h) * kDeltaDim + dv0) * kDeltaDim + lane * 4;
 
+  // a token's inputs, asked for one token ahead
+  const int hk = h / (a.hv / a.hk);
+  struct Token {
+    uint2 k, q;
+    __nv_bfloat16 v;
+    float g, beta;
+  };
+  auto fetch = [&](int t) {
+    const int64_t row = row0 + t;
+    Token x;
+    x.k = __ldg(reinterpret_cast<const uint2*>(a.k + row * a.k_stride + hk * kDeltaDim) + lane);
+    x.q = __ldg(reinterpret_cast<const uint2*>(a.q + row * a.q_stride + hk * kDeltaDim) + lane);
+    x.v = a.v[row * a.v_stride + (int64_t)h * kDeltaDim + dv0 + (lane & 15)];
+    x.g = __ldg(a.g + row * a.hv + h);
+    x.beta = __ldg(a.beta + row * a.hv + h);
+    return x;
+  };
+  Token next = {};
+  if (n > 0) next = fetch(0);
+
   float4 s[kRecRows];
   if (a.state_in && slot >= 0) {
 #pragma unroll
@@ -105,16 +125,13 @@ __global__ void __launch_bounds__(kRecWarps * 32) delta_recurrent_kernel(const D
     for (int r = 0; r < kRecRows; ++r) s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 
-  const int hk = h / (a.hv / a.hk);
   for (int t = 0; t < n; ++t) {
     const int64_t row = row0 + t;
-    const uint2 kr = __ldg(reinterpret_cast<const uint2*>(a.k + row * a.k_stride + hk * kDeltaDim) + lane);
-    const uint2 qr = __ldg(reinterpret_cast<const uint2*>(a.q + row * a.q_stride + hk * kDeltaDim) + lane);
-    const float vv = __bfloat162float(a.v[row * a.v_stride + (int64_t)h * kDeltaDim + dv0 + (lane & 15)]);
-    const float alpha = expf(__ldg(a.g + row * a.hv + h));
-    const float beta = __ldg(a.beta + row * a.hv + h);
-    float k[4] = {bf16_lo(kr.x), bf16_hi(kr.x), bf16_lo(kr.y), bf16_hi(kr.y)};
-    float q[4] = {bf16_lo(qr.x), bf16_hi(qr.x), bf16_lo(qr.y), bf16_hi(qr.y)};
+    const Token x = next;
+    if (t + 1 < n) next = fetch(t + 1);
+    const float vv = __bfloat162float(x.v), alpha = expf(x.g), beta = x.beta;
+    float k[4] = {bf16_lo(x.k.x), bf16_hi(x.k.x), bf16_lo(x.k.y), bf16_hi(x.k.y)};
+    float q[4] = {bf16_lo(x.q.x), bf16_hi(x.q.x), bf16_lo(x.q.y), bf16_hi(x.q.y)};
     float kk = 0.f, qq = 0.f, kq = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

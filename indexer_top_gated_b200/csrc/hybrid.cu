@@ -296,7 +296,7 @@ namespace dsa {
 namespace {
 
 // Sequences of up to this many tokens run token by token.
-constexpr int kDeltaShort = 16;
+constexpr int kDeltaShort = 24;
 
 dsa_status check_delta(const dsa_delta_params* P, const dsa_ragged* R) {
   DSA_TRY(check_rows(R));

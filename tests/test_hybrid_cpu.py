@@ -168,7 +168,7 @@ def test_delta_workspace(dsa):
     # per chunk and head: three pieces of the inverse and P, ten 16 x 16 bf16 blocks each, and the
     # scalars
     assert mn == (3000 // 64 + 3) * (4 * 10 * 512 + 1024) and rec == 4 * mn
-    assert dsa.dsa_gated_delta_workspace_size(shape, _rg(dsa, batch=3, q=16)) == (0, 0)
+    assert dsa.dsa_gated_delta_workspace_size(shape, _rg(dsa, batch=3, q=24)) == (0, 0)
     W = dsa.DSA_ERR_WORKSPACE
     assert _delta(dsa, ws=None) == W
     assert _delta(dsa, ws=_at(9) + 16) == W
