@@ -211,8 +211,9 @@ dsa_status dsa_rope_append(const dsa_params* P, const dsa_ragged* R, const dsa_r
   HybridDevice dev;
   DSA_TRY(hybrid_device(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // one row per CTA until there are CTAs enough to fill the GPU several times over
-  if (R->total_q < (int64_t)dev.num_sms * 32)
+  // One row per CTA for few rows (64 rows 4.4 us, by four 6.1 us; 592 rows 7.3 and 6.9 us, 4736
+  // rows 57 and 43 us)
+  if (R->total_q < (int64_t)dev.num_sms * 3)
     rope_append_kernel<1><<<(unsigned)R->total_q, kRopeThreads, 0, st>>>(a);
   else
     rope_append_kernel<4><<<(unsigned)((R->total_q + 3) / 4), kRopeThreads, 0, st>>>(a);
@@ -229,8 +230,10 @@ constexpr int kConvRun = 48;  // rows of a run in a large batch
 template <int W>
 dsa_status launch_conv(const ConvArgs& a, const dsa_ragged* R, int sms, cudaStream_t st) {
   const int groups = (a.channels / 8 + kConvThreads - 1) / kConvThreads;
-  // long runs read fewer rows twice; short ones spread a small batch over the GPU
-  const bool wide = R->total_q / kConvRun * groups >= 4 * (int64_t)sms;
+  // Long runs read fewer rows twice; short ones spread a small batch over the GPU (8192 channels,
+  // runs of 8 and of 48 rows: 300 rows 6.7 and 13.0 us, 1500 rows 16.4 and 14.9 us, 8000 rows 91
+  // and 65 us)
+  const bool wide = R->total_q / kConvRun * groups * 2 >= 3 * (int64_t)sms;
   const bool single = R->max_q_len <= 1;
   const int64_t runs = single ? R->batch : R->total_q / (wide ? kConvRun : 8) + R->batch;
   const unsigned y = (unsigned)std::min<int64_t>(runs, 32768);
@@ -295,7 +298,8 @@ dsa_status dsa_short_conv(const dsa_conv_params* P, const dsa_ragged* R, const v
 namespace dsa {
 namespace {
 
-// Sequences of up to this many tokens run token by token.
+// Sequences of up to this many tokens run token by token (at 24 tokens, against the chunks: 16
+// sequences x 16 heads 61 and 68 us, 64 x 32 281 and 346 us; the cost grows with each token).
 constexpr int kDeltaShort = 24;
 
 dsa_status check_delta(const dsa_delta_params* P, const dsa_ragged* R) {
@@ -433,18 +437,21 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   for (int h0 = 0; h0 < a.hv; h0 += (int)pass) {
     a.head0 = h0;
     a.heads = (int)std::min<int64_t>(pass, a.hv - h0);
-    // value heads of one key head together, where a pass is whole groups of them and CTAs abound
+    // The value heads of a key head in one preparation CTA, where a pass is whole groups of them
+    // and enough CTAs remain (4 key and 16 value heads, apart and together: 2048 tokens 102 and
+    // 110 us the whole call, 8192 tokens 291 and 284 us, 32768 tokens 1047 and 1012 us)
     const int group = a.hv / a.hk;
     const bool whole = h0 % group == 0 && a.heads % group == 0;
-    a.per_cta = whole && slots * (a.heads / group) >= 8 * (int64_t)dev.num_sms ? group : 1;
+    a.per_cta = whole && slots * (a.heads / group) >= 3 * (int64_t)dev.num_sms ? group : 1;
     const unsigned ctas = (unsigned)(slots * (a.heads / a.per_cta));
     if (a.per_cta > 1)
       delta_prep_kernel<true><<<ctas, kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
     else
       delta_prep_kernel<false><<<ctas, kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
     DSA_TRY(launched("delta_prep_kernel"));
-    // 16 value columns a CTA while those CTAs fit the GPU at once: a pair of chain warps alone on
-    // an SM is faster (XXX)
+    // 16 value columns a CTA while those CTAs fit the GPU at once: the schedulers of an SM then
+    // carry one warp each (4096 tokens, 16 and 32 columns: 8 heads 148 and 179 us, 18 heads 159
+    // and 188 us, 20 heads 264 and 194 us)
     if ((int64_t)a.batch * a.heads * ScanGeo<1>::kParts <= dev.num_sms)
       DSA_TRY(launch_scan<1>(a, maps, st));
     else
