@@ -333,16 +333,4 @@ DSA_DEV int seq_of_row(const int32_t* __restrict__ offs, int batch, int64_t r) {
   return lo;
 }
 
-// Sequence that owns packed query row r, found by the whole CTA (every thread calls it): one
-// round of loads in place of a chain of dependent ones.
-template <int THREADS>
-DSA_DEV int seq_of_row_cta(const int32_t* __restrict__ offs, int batch, int64_t r) {
-  int b = 0;
-  for (int i = 1; i < batch; i += THREADS) {
-    const int at = i + (int)threadIdx.x;
-    b += __syncthreads_count(at < batch && (int64_t)__ldg(offs + at) <= r);
-  }
-  return b;
-}
-
 }  // namespace dsa
