@@ -399,8 +399,8 @@ dsa_status dsa_decode_noalloc(const dsa_params* params, const dsa_ragged* ragged
  * the rows of the caches, and dsa_short_conv + dsa_gated_delta_prefill / _decode compute the
  * linear branch, `other` of dsa_sparse_attn_gated_mix.  The pages name both and define neither;
  * the formulas below are the ones this library implements.
- * The conventions at the top hold; rows of a padded batch (q_offsets[batch] .. total_q-1) are
- * neither read nor written.
+ * The conventions at the top hold.  Rows of a padded batch (q_offsets[batch] .. total_q-1) enter
+ * no result and are not written.
  */
 
 /* Pairs of a rotated part of r dimensions: (i, i + r/2), or (2i, 2i + 1). */
@@ -472,7 +472,8 @@ typedef struct {
  * Angles are formed and reduced in 64 bits; the rotation is fp32, rounded once.
  * Supported: head_dim 128, idx_dim 64, 1 .. 4 indexer heads, any Hq and Hkv; rotated
  * dimensions a multiple of 16, their offset a multiple of 8.  Of dsa_params only the head
- * counts and dimensions, idx_dtype and idx_scale_* are read (those of absent inputs are not).
+ * counts and dimensions, idx_dtype and idx_scale_* are read (counts and scales of absent inputs
+ * are not).
  * Requirements: every buffer 16-byte aligned, row strides multiples of 8; an output overlaps
  * nothing else in the call but, exactly, its own packed input; positions of one sequence's
  * rows do not share cache rows with another's new rows.
@@ -505,7 +506,8 @@ typedef struct {
  *               n_states-1 starts from zeros and its state is not kept.
  * Sums are fp32, the output is rounded once.  Only batch, q_offsets and total_q of dsa_ragged
  * are read.  Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps
- * neither x nor a state; state_out is state_in or does not overlap it.
+ * neither x, the weights nor a state; state_out is state_in or does not overlap it, nor anything
+ * else.
  */
 dsa_status dsa_short_conv(const dsa_conv_params* params, const dsa_ragged* ragged, const void* x,
                           const void* weight, const void* bias, const void* state_in,

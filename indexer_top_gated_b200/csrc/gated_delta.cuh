@@ -31,6 +31,7 @@
 #include <cstddef>
 
 #include "common.cuh"
+#include "find_last.cuh"
 
 namespace dsa {
 
@@ -356,9 +357,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
   const int groups = kGroup ? a.heads / a.per_cta : a.heads;
   const int64_t slot = blockIdx.x / groups;
   const int hl0 = (int)(blockIdx.x % groups) * (kGroup ? a.per_cta : 1);  // first of its value heads
-  int lo = 0;  // the sequence whose slots hold this one
-  for (int i = 1; i < a.batch; i += kPrepThreads)
-    lo += __syncthreads_count(i + tid < a.batch && delta_first_slot(a, i + tid) <= slot);
+  // the sequence whose slots hold this one
+  const int lo =
+      find_last<kPrepThreads>(a.batch, [&](int b) { return delta_first_slot(a, b) <= slot; });
   const int64_t first = __ldg(a.q_offsets + lo), end = __ldg(a.q_offsets + lo + 1);
   const int64_t row0 = first + (slot - delta_first_slot(a, lo)) * kDeltaChunk;
   if (end - first < a.min_len || row0 >= end) return;

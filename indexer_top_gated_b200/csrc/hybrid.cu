@@ -134,13 +134,14 @@ dsa_status dsa_rope_append(const dsa_params* P, const dsa_ragged* R, const dsa_r
     DSA_TRY(check_rot(O->rot_dim, O->rot_offset, 128));
     if ((B->q && P->n_q_heads < 1) || ((B->k || B->v) && P->n_kv_heads < 1))
       return DSA_ERR_INVALID_ARG;
-    if (P->n_q_heads > 65536 || P->n_kv_heads > 65536) return DSA_ERR_UNSUPPORTED;
+    if ((B->q && P->n_q_heads > 65536) || ((B->k || B->v) && P->n_kv_heads > 65536))
+      return DSA_ERR_UNSUPPORTED;
   }
   if (idx) {
     if (P->idx_dim != 64 || P->n_idx_heads < 1 || P->n_idx_heads > 4) return DSA_ERR_UNSUPPORTED;
     if (P->idx_dtype != DSA_BF16 && P->idx_dtype != DSA_FP8_E4M3) return DSA_ERR_INVALID_ARG;
-    if (!(P->idx_scale_q > 0.f) || !(P->idx_scale_k > 0.f) || !std::isfinite(P->idx_scale_q) ||
-        !std::isfinite(P->idx_scale_k))
+    if ((B->q_idx && (!(P->idx_scale_q > 0.f) || !std::isfinite(P->idx_scale_q))) ||
+        (B->k_idx && (!(P->idx_scale_k > 0.f) || !std::isfinite(P->idx_scale_k))))
       return DSA_ERR_INVALID_ARG;
     DSA_TRY(check_rot(O->idx_rot_dim, O->idx_rot_offset, 64));
   }
@@ -269,7 +270,10 @@ dsa_status dsa_short_conv(const dsa_conv_params* P, const dsa_ragged* R, const v
   const Span sx = span(x, R->total_q, a.x_stride, P->channels, 2);
   const Span s0 = span(state_in, P->n_states, slot, slot, 2);
   const Span s1 = span(state_out, P->n_states, slot, slot, 2);
-  if (overlap(so, sx) || overlap(so, s0) || overlap(so, s1) || overlap(sx, s1))
+  const Span sw = span(weight, 1, 0, (int64_t)P->channels * P->width, 2);
+  const Span sb = span(bias, 1, 0, P->channels, 2);
+  if (overlap(so, sx) || overlap(so, s0) || overlap(so, s1) || overlap(sx, s1) ||
+      overlap(so, sw) || overlap(so, sb) || overlap(s1, sw) || overlap(s1, sb))
     return DSA_ERR_INVALID_ARG;
   if (state_in != state_out && overlap(s0, s1)) return DSA_ERR_INVALID_ARG;
   a.q_offsets = R->q_offsets;
@@ -309,6 +313,8 @@ dsa_status check_delta(const dsa_delta_params* P, const dsa_ragged* R) {
   if (P->n_k_heads < 1 || P->n_v_heads < 1 || P->n_v_heads % P->n_k_heads != 0)
     return DSA_ERR_INVALID_ARG;
   if (P->n_v_heads > 65536) return DSA_ERR_UNSUPPORTED;
+  // (a CTA of the scan takes 16 or more of a head's 128 value columns)
+  if ((int64_t)R->batch * P->n_v_heads * 8 > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   if (P->reserved != 0 || P->n_states < 0) return DSA_ERR_INVALID_ARG;
   if (P->qk_norm && (!(P->norm_eps > 0.f) || !std::isfinite(P->norm_eps)))
     return DSA_ERR_INVALID_ARG;
@@ -366,7 +372,6 @@ dsa_status launch_recurrent(DeltaArgs a, int max_len, cudaStream_t st) {
   a.min_len = 0;
   a.max_len = max_len;
   const int64_t ctas = (int64_t)a.batch * a.hv * kRecParts;
-  if (ctas > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   delta_recurrent_kernel<<<(unsigned)ctas, kRecWarps * 32, 0, st>>>(a);
   return launched("delta_recurrent_kernel");
 }
@@ -375,7 +380,6 @@ template <int PAIRS>
 dsa_status launch_scan(const DeltaArgs& a, const DeltaMaps& maps, cudaStream_t st) {
   using Geo = ScanGeo<PAIRS>;
   const int64_t ctas = (int64_t)a.batch * a.heads * Geo::kParts;
-  if (ctas > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   delta_scan_kernel<PAIRS><<<(unsigned)ctas, Geo::kThreads, Geo::kSmem, st>>>(a, maps);
   return launched("delta_scan_kernel");
 }

@@ -10,24 +10,13 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "find_last.cuh"
 
 namespace dsa {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopePairs = 64;     // pairs of an attention head of 128, at most
 constexpr int kRopeIdxPairs = 32;  // pairs of an indexer head of 64, at most
-
-// Sequence that owns packed query row r, found by the whole CTA (every thread calls it): one
-// round of loads in place of a chain of dependent ones.
-template <int THREADS>
-DSA_DEV int seq_of_row_cta(const int32_t* __restrict__ offs, int batch, int64_t r) {
-  int b = 0;
-  for (int i = 1; i < batch; i += THREADS) {
-    const int at = i + (int)threadIdx.x;
-    b += __syncthreads_count(at < batch && (int64_t)__ldg(offs + at) <= r);
-  }
-  return b;
-}
 
 struct RopeTensor {
   const __nv_bfloat16* src;
@@ -208,7 +197,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const __gr
     cp_async_commit();
   }
 
-  const int b0 = seq_of_row_cta<kRopeThreads>(a.q_offsets, a.batch, r0);
+  const int b0 = find_last<kRopeThreads>(
+      a.batch, [&](int b) { return (int64_t)__ldg(a.q_offsets + b) <= r0; });
   if (tid < n) {
     const int64_t r = r0 + tid;
     int64_t q_row = -1, c_row = -1;

@@ -7,6 +7,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "find_last.cuh"
 
 namespace dsa {
 
@@ -56,10 +57,8 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
     if (run >= a.batch) return;
     b = (int)run;
   } else {
-    for (int i = 1; i < a.batch; i += kConvThreads) {
-      const int at = i + threadIdx.x;
-      b += __syncthreads_count(at < a.batch && __ldg(a.q_offsets + at) / RUN + at <= run);
-    }
+    b = find_last<kConvThreads>(
+        a.batch, [&](int i) { return __ldg(a.q_offsets + i) / RUN + (int64_t)i <= run; });
   }
   if (c0 >= a.channels) return;
   const int64_t first = __ldg(a.q_offsets + b);

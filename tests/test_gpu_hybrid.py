@@ -639,6 +639,29 @@ def test_binding_refuses_what_the_library_cannot_see():
         dsa.dsa_gated_delta_prefill(d.shape, d.rg, **dict(good, q=_randn(0, 20, 2, 256)[..., ::2]))
 
 
+# ---------------------------------------------------------------- many sequences
+
+def test_batches_of_thousands_of_sequences():
+    """More sequences than a block-wide search reads at once, empty ones among them."""
+    rng = np.random.default_rng(3)
+    lens = [int(n) for n in rng.integers(0, 4, 1500)]
+    lens[700], lens[1499] = 70, 26
+    rope = dsa.RopeShape()
+    t = _Rope(lens, [int(h) for h in rng.integers(0, 9, 1500)], heads=(2, 1, 1))
+    t.call(rope)
+    t.check(rope)
+    n, c, w = sum(lens), 64, 4
+    x, weight = _randn(1, n, c), _randn(2, c, w)
+    out, st = torch.empty_like(x), torch.empty(len(lens), w - 1, c, dtype=BF16, device="cuda")
+    off = _offsets(lens)
+    dsa.dsa_short_conv(dsa.ConvShape(c, w), dsa.ragged(off, off, lens, lens), x, weight, out, state_out=st)
+    ref, mag, states = _conv_ref(x, lens, weight, None, True, None, None, len(lens))
+    _near(out, ref, U * ref.abs() + 2.0 ** -20 * 1.1 * mag, "out")
+    assert torch.equal(st.double().cpu(), torch.stack([states[s] for s in range(len(lens))]))
+    d = _Delta(lens, 1, 1)
+    d.check(*d.call())
+
+
 # ---------------------------------------------------------------- a run of them together
 
 def test_hybrid_layer_end_to_end():

@@ -116,6 +116,8 @@ def test_conv_refusals(dsa):
     assert _conv(dsa, ptrs=dict(out=_at(0))) == inv                # a row's window is read after it
     assert _conv(dsa, ptrs=dict(state_out=_at(3) + 16)) == inv     # shifted over state_in
     assert _conv(dsa, ptrs=dict(out=_at(4))) == inv
+    for name in ("out", "state_out"):                              # over the weights, the bias
+        assert _conv(dsa, ptrs={name: _at(1)}) == inv and _conv(dsa, ptrs={name: _at(2)}) == inv
     assert _conv(dsa, rg=_rg(dsa, batch=0)) == inv
     assert dsa.lib.dsa_short_conv(None, ctypes.byref(_rg(dsa)), *([_at(0)] * 7), None) == inv
 
@@ -155,6 +157,22 @@ def test_delta_refusals(dsa, decode):
         assert call(ptrs=dict(out=_at(at))) == inv, name
     assert call(ptrs=dict(state_out=_at(5) + 128 * 128 * 4)) == inv
     assert call(rg=_rg(dsa, q=1, q_offsets=None)) == inv
+
+
+def test_absent_inputs_are_not_checked(dsa):
+    """Rotary append of q alone: the other heads' counts and the indexer's scales say nothing."""
+    only_q = {n: None for n, _ in dsa.RopeBuffers._fields_ if n not in ("q", "q_out")}
+    shape = dsa.LayerShape(top_k=4, n_kv_heads=-5, idx_dim=7, idx_scale_q=0.0)
+    rg = _rg(dsa, total_q=0)
+    assert _rope(dsa, rg=rg, shape=shape, buffers=only_q) == 0
+    shape = dsa.LayerShape(top_k=4, n_q_heads=1 << 20)
+    assert _rope(dsa, rg=rg, shape=shape, buffers=only_q) == dsa.DSA_ERR_UNSUPPORTED
+
+
+def test_delta_batches_too_large(dsa):
+    big = _rg(dsa, batch=1 << 24, q=1)
+    assert _delta(dsa, decode=True, rg=big, n_v_heads=64, n_k_heads=64) == dsa.DSA_ERR_UNSUPPORTED
+    assert _delta(dsa, rg=big, n_v_heads=64, n_k_heads=64) == dsa.DSA_ERR_UNSUPPORTED
 
 
 def test_delta_decode_is_one_token_per_sequence(dsa):
