@@ -290,7 +290,7 @@ struct PrepSmem {
     };
     float A[kDeltaChunk * kPrepLd];  // once the products are in registers
   };
-  alignas(16) float2 G[kDeltaChunk];  // running sum of g, high and low part
+  alignas(16) float2 G[kDeltaChunk];  // running sum of g log2(e), high and low part
   alignas(16) float ink[kDeltaChunk], inq[kDeltaChunk], beta[kDeltaChunk];
   uint64_t bar;
   int abort;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
   }
   auto gates = [&](int h) {
     if (warp == 0) {
-      // running sum of g, two tokens a lane, in fp64 and then as a pair of fp32.  -inf (alpha = 0)
+      // running sum of g log2(e), two tokens a lane, in fp64 and then as a pair of fp32.  -inf (alpha = 0)
       // becomes a finite decay that is 0 all the same, so that differences of sums behind it stay
       // numbers.
       double x[2];
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
       for (int i = 0; i < 2; ++i) {
         const int t = lane * 2 + i;
         const float g = t < valid ? __ldg(a.g + (row0 + t) * a.hv + h) : 0.f;
-        x[i] = g < -1e5f ? -1e5 : (double)g;
+        x[i] = (g < -1e5f ? -1e5 : (double)g) * 1.4426950408889634;
       }
       double sum = x[0] + x[1];
       const double own = sum;
@@ -489,33 +489,57 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
   if (tid < 64) {
     float* scal = reinterpret_cast<float*>(dst + kDeltaScal);
     const float2 g = sm.G[tid], ge = sm.G[63];
-    const float eg = expf(g.x + g.y);
+    const float eg = exp2f(g.x + g.y);
     scal[tid] = eg * sm.ink[tid];
-    scal[64 + tid] = expf((ge.x - g.x) + (ge.y - g.y)) * sm.ink[tid];
+    scal[64 + tid] = exp2f((ge.x - g.x) + (ge.y - g.y)) * sm.ink[tid];
     scal[128 + tid] = a.scale * eg * sm.inq[tid];
-    if (tid == 0) scal[192] = expf(ge.x + ge.y);
+    if (tid == 0) scal[192] = exp2f(ge.x + ge.y);
   }
+  // this lane's two rows of either row tile
+  float2 gi[2][2];
+  float fa[2][2], fp[2][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int i = (m ? mt_b : mt_a) * 16 + (lane >> 2) + half * 8;
+      gi[m][half] = sm.G[i];
+      fa[m][half] = sm.beta[i] * sm.ink[i];
+      fp[m][half] = a.scale * sm.inq[i];
+    }
 #pragma unroll
   for (int t = 0; t < 5; ++t) {
-    const int mt = t < n_a ? mt_a : mt_b, nt = t < n_a ? nt0 + t : t - n_a;
+    const bool second = t >= n_a;
+    const int mt = second ? mt_b : mt_a, nt = second ? t - n_a : nt0 + t;
     const int j = nt * 8 + (lane & 3) * 2;
     const float4 gj = *reinterpret_cast<const float4*>(sm.G + j);
     const float2 ik = *reinterpret_cast<const float2*>(sm.ink + j);
+    const bool diagonal = (nt >> 1) == mt;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = mt * 16 + (lane >> 2) + half * 8;
-      const float2 gi = sm.G[i];
-      const float fa = sm.beta[i] * sm.ink[i], fp = a.scale * sm.inq[i];
+      const float2 g = second ? gi[1][half] : gi[0][half];
+      const float ra = second ? fa[1][half] : fa[0][half], rp = second ? fp[1][half] : fp[0][half];
       // e^(G_i - G_j): the high parts cancel exactly where it matters
-      const float d0 = j <= i ? __expf((gi.x - gj.x) + (gi.y - gj.y)) * ik.x : 0.f;
-      const float d1 = j < i ? __expf((gi.x - gj.z) + (gi.y - gj.w)) * ik.y : 0.f;
-      float2 x;
-      x.x = j < i ? fa * d0 * kk[t][half * 2] : 0.f;
-      x.y = j + 1 < i ? fa * d1 * kk[t][half * 2 + 1] : 0.f;
+      float x0 = (g.x - gj.x) + (g.y - gj.y), x1 = (g.x - gj.z) + (g.y - gj.w);
+      if (diagonal) {  // e^-inf = 0 right of the diagonal
+        if (j > i) x0 = -INFINITY;
+        if (j >= i) x1 = -INFINITY;
+      }
+      const float d0 = ex2_approx(x0) * ik.x, d1 = ex2_approx(x1) * ik.y;
+      float2 x = make_float2(ra * d0 * kk[t][half * 2], ra * d1 * kk[t][half * 2 + 1]);
+      if (diagonal) {
+        if (j >= i) x.x = 0.f;
+        if (j + 1 >= i) x.y = 0.f;
+      }
       *reinterpret_cast<float2*>(sm.A + i * kPrepLd + j) = x;
+      float2 y = make_float2(rp * d0 * qk[t][half * 2], rp * d1 * qk[t][half * 2 + 1]);
+      if (diagonal) {  // (not 0 times a product that may not be a number)
+        if (j > i) y.x = 0.f;
+        if (j >= i) y.y = 0.f;
+      }
       *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + tri_unit(i, nt) + (lane & 3) * 4) =
-          pack_bf16x2(j <= i ? fp * d0 * qk[t][half * 2] : 0.f,
-                      j < i ? fp * d1 * qk[t][half * 2 + 1] : 0.f);
+          pack_bf16x2(y.x, y.y);
     }
   }
   if (tid < 64) {  // above the diagonal inside the 32 x 32 blocks
