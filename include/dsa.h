@@ -541,7 +541,9 @@ typedef struct {
  * dsa_gated_delta_prefill takes any Q_b: sequences of up to 24 tokens run token by token, longer
  * ones in chunks of 64 (the state stays fp32; operands of the tensor-core products enter in
  * bf16 pieces that keep the state within about 1e-6 of itself).  A sequence's results depend
- * neither on the rest of the batch nor on the workspace's size.
+ * neither on the rest of the batch nor on the workspace's size.  A NaN or an infinity in a token's
+ * inputs stays in its sequence and value heads, but within its chunk of 64 it may reach the outputs
+ * of tokens before it.
  * dsa_gated_delta_decode is for at most one token per sequence (max_q_len <= 1) and takes no
  * workspace.
  *   workspace   device, 256-byte aligned, ws_bytes >= the minimum of
