@@ -8,7 +8,8 @@
 //
 // Recurrent form (delta_recurrent_kernel): decode and sequences of few tokens.  What it cannot
 // do without is the state, 64 KB a head in and out; a warp keeps 16 rows of it in registers, so
-// the state crosses HBM once each way however many tokens the sequence has.
+// the state crosses HBM once each way however many tokens the sequence has.  Measured: 256
+// sequences x 64 heads 326 us, 6.6 TB/s; 64 x 32 heads 44 us, 6.1 TB/s.
 //
 // Chunked form: with G the running sum of g inside a chunk of 64 tokens,
 //   (I + A) U = diag(beta) (V - diag(e^G) K S0^T),  A_ij = beta_i e^(G_i - G_j) k_i.k_j (j < i)
@@ -17,7 +18,7 @@
 // delta_prep_kernel computes what does not depend on the state, for every chunk at once:
 // T = (I + A)^-1 diag(beta) and P = scale * tril(Q K^T) . e^(G_i - G_j).  delta_scan_kernel then
 // walks a sequence's chunks with S in registers.  Columns of S^T (the dv axis) never meet, so
-// a CTA takes 32 or 64 of the 128, and a pair of warps 16 of them.
+// a CTA takes 32 or 16 of the 128, and a pair of warps 16 of them.
 //
 // Precision: the state, the norms, the decays and every sum are fp32 (the running sum of g
 // fp64, since only its differences matter and a strong decay leaves them small beside it).  The
@@ -279,7 +280,8 @@ DSA_DEV void split_frag(const float (&x)[4], const float (&y)[4], uint32_t (&f)[
 // fp32: its 16 x 16 diagonal blocks by forward substitution, and the blocks below by
 //   [T1 0; -T2 A21 T1, T2], twice, 16 -> 32 -> 64.
 // Written as loops rather than one unrolled substitution over 64 rows: that was bound by
-// instruction fetch.
+// instruction fetch.  Measured: 8192 tokens x 32 heads about 80 us (from 158); no pipe is above
+// 57 %, waits and barriers of short dependent phases bound it.
 constexpr int kPrepThreads = 128;
 constexpr int kPrepLd = 68;  // floats per row of A: 16-byte rows, eight rows on distinct banks
 
@@ -377,9 +379,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
   }
   auto gates = [&](int h) {
     if (warp == 0) {
-      // running sum of g log2(e), two tokens a lane, in fp64 and then as a pair of fp32.  -inf (alpha = 0)
-      // becomes a finite decay that is 0 all the same, so that differences of sums behind it stay
-      // numbers.
+      // running sum of g log2(e), two tokens a lane, in fp64 and then as a pair of fp32.  -inf
+      // (alpha = 0) becomes a finite decay that is 0 all the same, so that differences of sums
+      // behind it stay numbers.
       double x[2];
   #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -483,170 +485,170 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
   const int per = kGroup ? a.per_cta : 1;
 #pragma unroll 1
   for (int hl = hl0; hl < hl0 + per; ++hl) {
-  __syncthreads();  // gates and norms are there; K's and Q's tiles, or the last head's A, are free
+    __syncthreads();  // gates and norms are there; K's and Q's tiles, or the last head's A, are free
 
-  unsigned char* dst = a.ws + (slot * a.heads + hl) * kDeltaItemBytes;
-  if (tid < 64) {
-    float* scal = reinterpret_cast<float*>(dst + kDeltaScal);
-    const float2 g = sm.G[tid], ge = sm.G[63];
-    const float eg = exp2f(g.x + g.y);
-    scal[tid] = eg * sm.ink[tid];
-    scal[64 + tid] = exp2f((ge.x - g.x) + (ge.y - g.y)) * sm.ink[tid];
-    scal[128 + tid] = a.scale * eg * sm.inq[tid];
-    if (tid == 0) scal[192] = exp2f(ge.x + ge.y);
-  }
-  // this lane's two rows of either row tile
-  float2 gi[2][2];
-  float fa[2][2], fp[2][2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int i = (m ? mt_b : mt_a) * 16 + (lane >> 2) + half * 8;
-      gi[m][half] = sm.G[i];
-      fa[m][half] = sm.beta[i] * sm.ink[i];
-      fp[m][half] = a.scale * sm.inq[i];
+    unsigned char* dst = a.ws + (slot * a.heads + hl) * kDeltaItemBytes;
+    if (tid < 64) {
+      float* scal = reinterpret_cast<float*>(dst + kDeltaScal);
+      const float2 g = sm.G[tid], ge = sm.G[63];
+      const float eg = exp2f(g.x + g.y);
+      scal[tid] = eg * sm.ink[tid];
+      scal[64 + tid] = exp2f((ge.x - g.x) + (ge.y - g.y)) * sm.ink[tid];
+      scal[128 + tid] = a.scale * eg * sm.inq[tid];
+      if (tid == 0) scal[192] = exp2f(ge.x + ge.y);
     }
+    // this lane's two rows of either row tile
+    float2 gi[2][2];
+    float fa[2][2], fp[2][2];
 #pragma unroll
-  for (int t = 0; t < 5; ++t) {
-    const bool second = t >= n_a;
-    const int mt = second ? mt_b : mt_a, nt = second ? t - n_a : nt0 + t;
-    const int j = nt * 8 + (lane & 3) * 2;
-    const float4 gj = *reinterpret_cast<const float4*>(sm.G + j);
-    const float2 ik = *reinterpret_cast<const float2*>(sm.ink + j);
-    const bool diagonal = (nt >> 1) == mt;
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int i = mt * 16 + (lane >> 2) + half * 8;
-      const float2 g = second ? gi[1][half] : gi[0][half];
-      const float ra = second ? fa[1][half] : fa[0][half], rp = second ? fp[1][half] : fp[0][half];
-      // e^(G_i - G_j): the high parts cancel exactly where it matters
-      float x0 = (g.x - gj.x) + (g.y - gj.y), x1 = (g.x - gj.z) + (g.y - gj.w);
-      if (diagonal) {  // e^-inf = 0 right of the diagonal
-        if (j > i) x0 = -INFINITY;
-        if (j >= i) x1 = -INFINITY;
+      for (int half = 0; half < 2; ++half) {
+        const int i = (m ? mt_b : mt_a) * 16 + (lane >> 2) + half * 8;
+        gi[m][half] = sm.G[i];
+        fa[m][half] = sm.beta[i] * sm.ink[i];
+        fp[m][half] = a.scale * sm.inq[i];
       }
-      const float d0 = ex2_approx(x0) * ik.x, d1 = ex2_approx(x1) * ik.y;
-      float2 x = make_float2(ra * d0 * kk[t][half * 2], ra * d1 * kk[t][half * 2 + 1]);
-      if (diagonal) {
-        if (j >= i) x.x = 0.f;
-        if (j + 1 >= i) x.y = 0.f;
+#pragma unroll
+    for (int t = 0; t < 5; ++t) {
+      const bool second = t >= n_a;
+      const int mt = second ? mt_b : mt_a, nt = second ? t - n_a : nt0 + t;
+      const int j = nt * 8 + (lane & 3) * 2;
+      const float4 gj = *reinterpret_cast<const float4*>(sm.G + j);
+      const float2 ik = *reinterpret_cast<const float2*>(sm.ink + j);
+      const bool diagonal = (nt >> 1) == mt;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int i = mt * 16 + (lane >> 2) + half * 8;
+        const float2 g = second ? gi[1][half] : gi[0][half];
+        const float ra = second ? fa[1][half] : fa[0][half], rp = second ? fp[1][half] : fp[0][half];
+        // e^(G_i - G_j): the high parts cancel exactly where it matters
+        float x0 = (g.x - gj.x) + (g.y - gj.y), x1 = (g.x - gj.z) + (g.y - gj.w);
+        if (diagonal) {  // e^-inf = 0 right of the diagonal
+          if (j > i) x0 = -INFINITY;
+          if (j >= i) x1 = -INFINITY;
+        }
+        const float d0 = ex2_approx(x0) * ik.x, d1 = ex2_approx(x1) * ik.y;
+        float2 x = make_float2(ra * d0 * kk[t][half * 2], ra * d1 * kk[t][half * 2 + 1]);
+        if (diagonal) {
+          if (j >= i) x.x = 0.f;
+          if (j + 1 >= i) x.y = 0.f;
+        }
+        *reinterpret_cast<float2*>(sm.A + i * kPrepLd + j) = x;
+        float2 y = make_float2(rp * d0 * qk[t][half * 2], rp * d1 * qk[t][half * 2 + 1]);
+        if (diagonal) {  // (not 0 times a product that may not be a number)
+          if (j > i) y.x = 0.f;
+          if (j >= i) y.y = 0.f;
+        }
+        *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + tri_unit(i, nt) + (lane & 3) * 4) =
+            pack_bf16x2(y.x, y.y);
       }
-      *reinterpret_cast<float2*>(sm.A + i * kPrepLd + j) = x;
-      float2 y = make_float2(rp * d0 * qk[t][half * 2], rp * d1 * qk[t][half * 2 + 1]);
-      if (diagonal) {  // (not 0 times a product that may not be a number)
-        if (j > i) y.x = 0.f;
-        if (j >= i) y.y = 0.f;
-      }
-      *reinterpret_cast<uint32_t*>(dst + 3 * kDeltaMat + tri_unit(i, nt) + (lane & 3) * 4) =
-          pack_bf16x2(y.x, y.y);
     }
-  }
-  if (tid < 64) {  // above the diagonal inside the 32 x 32 blocks
-    const int i = (tid >> 5) * 32 + (tid & 31) / 2, j = (tid >> 5) * 32 + 16 + (tid & 1) * 8;
-    *reinterpret_cast<float4*>(sm.A + i * kPrepLd + j) = make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(sm.A + i * kPrepLd + j + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __syncthreads();
-  {
-    // column c of the block's inverse: x_i = [i == c] - sum_{m < i} A_im x_m
-    const int c = lane & 15;
-    float* A = sm.A + warp * 16 * (kPrepLd + 1);
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int m = 0; m < i; m += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(A + i * kPrepLd + m);
-        s0 = fmaf(v.x, x[m], s0);
-        s1 = fmaf(v.y, x[m + 1], s1);
-        s0 = fmaf(v.z, x[m + 2], s0);
-        s1 = fmaf(v.w, x[m + 3], s1);
-      }
-      x[i] = (i == c ? 1.f : 0.f) - (s0 + s1);
+    if (tid < 64) {  // above the diagonal inside the 32 x 32 blocks
+      const int i = (tid >> 5) * 32 + (tid & 31) / 2, j = (tid >> 5) * 32 + 16 + (tid & 1) * 8;
+      *reinterpret_cast<float4*>(sm.A + i * kPrepLd + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(sm.A + i * kPrepLd + j + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __syncwarp();
-    if (lane < 16) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) A[i * kPrepLd + c] = x[i];
-    }
-  }
-  __syncthreads();
-  // The steps 16 -> 32 -> 64 on the tensor cores, transposed: Y = T1^T A21^T, then
-  // T21^T = -Y T2^T, Y going from accumulator to left operand in registers.  fp32 operands in
-  // three bf16 pieces, products below 2^-24 left out.  (As fp32 products out of shared memory
-  // these steps were half of the kernel's shared-memory traffic, which bounded it.)
-  const int part = warp & 1, half = warp >> 1;
-  {  // pair `part` of 16 x 16 blocks; rows 8 half .. of the block below
-    float* T1 = sm.A + part * 32 * (kPrepLd + 1);
-    float* A21 = T1 + 16 * kPrepLd;
-    float y[2][4] = {}, t[1][4] = {};
-    uint32_t fx[3][4], fb[2][3][2], f2[1][3][2];
-    prep_left(T1, fx);
-    prep_right(A21, fb[0]);
-    prep_right(A21 + 8 * kPrepLd, fb[1]);
-    prep_right(A21 + 16 + half * 8 * kPrepLd, f2[0]);
-    prep_mma(y, fx, fb);
-    split_frag<3>(y[0], y[1], fx);
-    prep_mma(t, fx, f2);
     __syncthreads();
-    prep_store(A21 + half * 8 * kPrepLd, t[0]);
-  }
-  __syncthreads();
-  {  // columns 16 part .. of the 32 x 32 block below, rows 16 half ..
-    float* A21 = sm.A + 32 * kPrepLd;
-    float y[4][4] = {}, t[2][4] = {};
-    uint32_t fx[3][4];
-    // T1 and T2 are lower triangular: rows 16 part .. of T1, and the first 16 (half + 1) of Y
-#pragma unroll 1
-    for (int kt = part; kt < 2; ++kt) {
-      uint32_t fb[4][3][2];
-      prep_left(sm.A + kt * 16 * kPrepLd + part * 16, fx);
+    {
+      // column c of the block's inverse: x_i = [i == c] - sum_{m < i} A_im x_m
+      const int c = lane & 15;
+      float* A = sm.A + warp * 16 * (kPrepLd + 1);
+      float x[16];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) prep_right(A21 + nt * 8 * kPrepLd + kt * 16, fb[nt]);
+      for (int i = 0; i < 16; ++i) x[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int m = 0; m < i; m += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(A + i * kPrepLd + m);
+          s0 = fmaf(v.x, x[m], s0);
+          s1 = fmaf(v.y, x[m + 1], s1);
+          s0 = fmaf(v.z, x[m + 2], s0);
+          s1 = fmaf(v.w, x[m + 3], s1);
+        }
+        x[i] = (i == c ? 1.f : 0.f) - (s0 + s1);
+      }
+      __syncwarp();
+      if (lane < 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) A[i * kPrepLd + c] = x[i];
+      }
+    }
+    __syncthreads();
+    // The steps 16 -> 32 -> 64 on the tensor cores, transposed: Y = T1^T A21^T, then
+    // T21^T = -Y T2^T, Y going from accumulator to left operand in registers.  fp32 operands in
+    // three bf16 pieces, products below 2^-24 left out.  (As fp32 products out of shared memory
+    // these steps were half of the kernel's shared-memory traffic, which bounded it.)
+    const int part = warp & 1, half = warp >> 1;
+    {  // pair `part` of 16 x 16 blocks; rows 8 half .. of the block below
+      float* T1 = sm.A + part * 32 * (kPrepLd + 1);
+      float* A21 = T1 + 16 * kPrepLd;
+      float y[2][4] = {}, t[1][4] = {};
+      uint32_t fx[3][4], fb[2][3][2], f2[1][3][2];
+      prep_left(T1, fx);
+      prep_right(A21, fb[0]);
+      prep_right(A21 + 8 * kPrepLd, fb[1]);
+      prep_right(A21 + 16 + half * 8 * kPrepLd, f2[0]);
       prep_mma(y, fx, fb);
-    }
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      if (kt > half) continue;
-      uint32_t fb[2][3][2];
-      split_frag<3>(y[2 * kt], y[2 * kt + 1], fx);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        prep_right(A21 + 32 + (half * 16 + e * 8) * kPrepLd + kt * 16, fb[e]);
-      prep_mma(t, fx, fb);
+      split_frag<3>(y[0], y[1], fx);
+      prep_mma(t, fx, f2);
+      __syncthreads();
+      prep_store(A21 + half * 8 * kPrepLd, t[0]);
     }
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 2; ++e) prep_store(A21 + (half * 16 + e * 8) * kPrepLd + part * 16, t[e]);
-  }
-  __syncthreads();
-  // T diag(beta) in three pieces, eight columns at a time
+    {  // columns 16 part .. of the 32 x 32 block below, rows 16 half ..
+      float* A21 = sm.A + 32 * kPrepLd;
+      float y[4][4] = {}, t[2][4] = {};
+      uint32_t fx[3][4];
+      // T1 and T2 are lower triangular: rows 16 part .. of T1, and the first 16 (half + 1) of Y
 #pragma unroll 1
-  for (int at = tid; at < kDeltaMat / 16; at += kPrepThreads) {
-    const int block = at >> 5, m = block >= 6 ? 3 : block >= 3 ? 2 : block >= 1 ? 1 : 0;
-    const int r = (at & 31) >> 1, unit = (at & 1) ^ ((r >> 2) & 1);
-    const int i = m * 16 + r, c = (block - ((m * (m + 1)) >> 1)) * 16 + unit * 8;
-    uint32_t p[4][3];
+      for (int kt = part; kt < 2; ++kt) {
+        uint32_t fb[4][3][2];
+        prep_left(sm.A + kt * 16 * kPrepLd + part * 16, fx);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4 t = *reinterpret_cast<const float4*>(sm.A + i * kPrepLd + c + e * 4);
-      const float4 w = *reinterpret_cast<const float4*>(sm.beta + c + e * 4);
-      split_pair<3>(t.x * w.x, t.y * w.y, p[2 * e]);
-      split_pair<3>(t.z * w.z, t.w * w.w, p[2 * e + 1]);
+        for (int nt = 0; nt < 4; ++nt) prep_right(A21 + nt * 8 * kPrepLd + kt * 16, fb[nt]);
+        prep_mma(y, fx, fb);
+      }
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        if (kt > half) continue;
+        uint32_t fb[2][3][2];
+        split_frag<3>(y[2 * kt], y[2 * kt + 1], fx);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          prep_right(A21 + 32 + (half * 16 + e * 8) * kPrepLd + kt * 16, fb[e]);
+        prep_mma(t, fx, fb);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) prep_store(A21 + (half * 16 + e * 8) * kPrepLd + part * 16, t[e]);
     }
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      *reinterpret_cast<uint4*>(dst + k * kDeltaMat + at * 16) =
-          make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
-  }
-  if (kGroup && hl + 1 < hl0 + per) {
     __syncthreads();
-    gates(a.head0 + hl + 1);
-  }
+    // T diag(beta) in three pieces, eight columns at a time
+#pragma unroll 1
+    for (int at = tid; at < kDeltaMat / 16; at += kPrepThreads) {
+      const int block = at >> 5, m = block >= 6 ? 3 : block >= 3 ? 2 : block >= 1 ? 1 : 0;
+      const int r = (at & 31) >> 1, unit = (at & 1) ^ ((r >> 2) & 1);
+      const int i = m * 16 + r, c = (block - ((m * (m + 1)) >> 1)) * 16 + unit * 8;
+      uint32_t p[4][3];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 t = *reinterpret_cast<const float4*>(sm.A + i * kPrepLd + c + e * 4);
+        const float4 w = *reinterpret_cast<const float4*>(sm.beta + c + e * 4);
+        split_pair<3>(t.x * w.x, t.y * w.y, p[2 * e]);
+        split_pair<3>(t.z * w.z, t.w * w.w, p[2 * e + 1]);
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint4*>(dst + k * kDeltaMat + at * 16) =
+            make_uint4(p[0][k], p[1][k], p[2][k], p[3][k]);
+    }
+    if (kGroup && hl + 1 < hl0 + per) {
+      __syncthreads();
+      gates(a.head0 + hl + 1);
+    }
   }
 }
 
@@ -665,7 +667,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
 // What bounds it: the chain's latency (220 tensor instructions a warp and chunk, which depend on
 // one another in four stages); the tensor pipe, which the output warps fill in the gaps, is the
 // next limit (304 a scheduler and chunk).  So accumulators alternate, eight or six between two
-// uses of one, and operands are fetched one step ahead.
+// uses of one, and operands are fetched one step ahead.  Measured: a chunk takes 1.65 us with one
+// set of warps a CTA (8 heads), 2.1 us with two (32 heads: tensor pipe 63 %, shared-memory pipe
+// 72 %); 32768 tokens x 32 heads 1.40 ms with the preparation.
 constexpr int kScanNV = 32;  // value columns of a V tile
 // one chunk's operands: K, Q, V, the workspace item
 constexpr int kScanV = 2 * kDeltaTile;
@@ -731,7 +735,8 @@ DSA_DEV void scan_loader(const DeltaArgs& a, const DeltaMaps& maps, const ScanPl
   const int n_chunks = (at.len + kDeltaChunk - 1) / kDeltaChunk;
   for (int c = 0; c < n_chunks; ++c) {
     const int valid = at.len - c * kDeltaChunk;
-    if (c >= 2) mbar_wait_bounded(smem_u32(&sy->empty[c & 1]), (c >> 1) + 1 & 1, a.status, &sy->abort);
+    if (c >= 2)
+      mbar_wait_bounded(smem_u32(&sy->empty[c & 1]), ((c >> 1) + 1) & 1, a.status, &sy->abort);
     const bool part = valid < kDeltaChunk;
     const uint32_t full = smem_u32(&sy->full[c & 1]);
     const uint32_t bar = part ? smem_u32(&sy->tail) : full;

@@ -2,8 +2,10 @@
 // is filtered over its own last W rows,
 //   y[t,c] = act(bias[c] + sum_{j < W} w[c,j] x[t - W + 1 + j, c]),
 // the rows before a sequence's first coming from its state (W - 1 rows, newest last).
-// Bound: HBM.  A thread walks kConvRun rows of 8 channels with the window in registers, so a row
-// is read once (and W - 1 rows again where a run begins).
+// Bound: HBM, closely followed by instruction issue (two exponentials and a reciprocal for two
+// activations).  A thread walks a run of rows of 8 channels (48, in small batches 8, 1 for single
+// tokens) with the window in registers, so a row is read once (and W - 1 rows again where a run
+// begins).  Measured: 32768 rows x 8192 channels 202 us, 5.3 TB/s.
 #pragma once
 
 #include "common.cuh"
