@@ -540,8 +540,10 @@ typedef struct {
  *   state_index int32 [batch] or NULL, as for dsa_short_conv.
  * dsa_gated_delta_prefill takes any Q_b: sequences of up to 24 tokens run token by token, longer
  * ones in chunks of 64 (the state stays fp32; operands of the tensor-core products enter in
- * bf16 pieces that keep the state within about 1e-6 of itself).  A sequence's results depend
- * neither on the rest of the batch nor on the workspace's size.  A NaN or an infinity in a token's
+ * bf16 pieces that keep the state within about 1e-6 of itself).  A sequence's results do not depend
+ * on the workspace's size, and on the rest of the batch only in the last bits, through the choice
+ * of the kernel: one for batches whose heads fill the GPU (total_q * n_v_heads against max_q_len),
+ * one for fewer.  A NaN or an infinity in a token's
  * inputs stays in its sequence and value heads, but within its chunk of 64 it may reach the outputs
  * of tokens before it.
  * dsa_gated_delta_decode is for at most one token per sequence (max_q_len <= 1) and takes no

@@ -16,7 +16,8 @@
 //   O = scale (diag(e^G) Q S0^T + (tril(Q K^T) . e^(G_i - G_j)) U)
 //   S = e^(G_C) S0 + U^T diag(e^(G_C - G_j)) K
 // delta_prep_kernel computes what does not depend on the state, for every chunk at once:
-// T = (I + A)^-1 diag(beta) and P = scale * tril(Q K^T) . e^(G_i - G_j).  delta_scan_kernel then
+// T = (I + A)^-1 diag(beta) and P = scale * tril(Q K^T) . e^(G_i - G_j).  delta_scan_kernel (or, for
+// batches that fill the GPU with whole heads, gated_delta_umma.cuh's) then
 // walks a sequence's chunks with S in registers.  Columns of S^T (the dv axis) never meet, so
 // a CTA takes 32 or 16 of the 128, and a pair of warps 16 of them.
 //
@@ -61,9 +62,9 @@ struct DeltaArgs {
 };
 
 // The rows of q, k and v as TMA sees them: boxes of 64 rows, 64 columns of q and k (128-byte
-// swizzle) and kScanNV of v (64-byte swizzle).
+// swizzle) and kScanNV = 32 of v and out (64-byte swizzle).
 struct DeltaMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, out;
 };
 
 // The state slot of sequence b, or -1: none (starts from zero, is not kept).
@@ -203,20 +204,20 @@ DSA_DEV int64_t delta_first_slot(const DeltaArgs& a, int b) {
   return (int64_t)__ldg(a.q_offsets + b) / kDeltaChunk + b;
 }
 
-// One item of the workspace, as the scan keeps it in shared memory: three pieces of T, P (bf16),
-// each the ten 16 x 16 blocks on and below the diagonal in row order, 512 bytes a block: 16 rows
-// of two 16-byte units, which trade places in rows 4 .. 7 and 12 .. 15 (ldmatrix then meets no
-// bank conflict); then the scalars of the tokens.
+// One item of the workspace: three pieces of T, P (bf16), each the ten 16 x 16 blocks on and below
+// the diagonal in column order, 512 bytes a block: 16 rows of two 16-byte units, which trade
+// places in rows 4 .. 7 and 12 .. 15 (ldmatrix then meets no bank conflict, and a column of blocks
+// is a K-major UMMA operand with 32-byte swizzle); then the scalars of the tokens.
 constexpr int kDeltaMat = 10 * 512;
 constexpr int kDeltaScal = 4 * kDeltaMat;        // a[64], t[64], b[64], e^(G_C)
 constexpr int kDeltaItemBytes = kDeltaScal + 1024;
 constexpr int kDeltaTile = kDeltaChunk * kDeltaDim * 2;  // K or Q of a chunk: two halves of the
                                                          // columns, rows of 128 bytes each
-// 16-byte unit of row r, columns 8 unit .. of the triangular matrices
+// From block (m, 0) of the triangular matrices to block (m, kt), and the 16-byte unit of row r,
+// columns 8 unit ..
+DSA_DEV constexpr int tri_col(int kt) { return kt * (7 - kt) / 2 * 512; }
 DSA_DEV int tri_unit(int r, int unit) {
-  const int m = r >> 4;
-  return (((m * (m + 1)) >> 1) + (unit >> 1)) * 512 + (r & 15) * 32 +
-         (((unit & 1) ^ ((r >> 2) & 1)) << 4);
+  return tri_col(unit >> 1) + r * 32 + (((unit & 1) ^ ((r >> 2) & 1)) << 4);
 }
 
 // 16-byte unit (columns 8 unit ..) of a row of a K or Q tile
@@ -629,9 +630,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
     // T diag(beta) in three pieces, eight columns at a time
 #pragma unroll 1
     for (int at = tid; at < kDeltaMat / 16; at += kPrepThreads) {
-      const int block = at >> 5, m = block >= 6 ? 3 : block >= 3 ? 2 : block >= 1 ? 1 : 0;
-      const int r = (at & 31) >> 1, unit = (at & 1) ^ ((r >> 2) & 1);
-      const int i = m * 16 + r, c = (block - ((m * (m + 1)) >> 1)) * 16 + unit * 8;
+      const int block = at >> 5, kt = block >= 9 ? 3 : block >= 7 ? 2 : block >= 4 ? 1 : 0;
+      const int i = (at - tri_col(kt) / 16) >> 1;
+      const int c = kt * 16 + ((at & 1) ^ ((i >> 2) & 1)) * 8;
       uint32_t p[4][3];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -879,7 +880,7 @@ DSA_DEV void scan_chain(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
     }
     auto load_t = [&](int own, int kt, uint32_t (&f)[3][4]) {
 #pragma unroll
-      for (int p = 0; p < 3; ++p) ldmatrix_x4(st + p * kDeltaMat + t_row[own] + kt * 512, f[p]);
+      for (int p = 0; p < 3; ++p) ldmatrix_x4(st + p * kDeltaMat + t_row[own] + tri_col(kt), f[p]);
     };
     load_t(0, tile[0], ft[0]);
     load_t(1, tile[0], ft[1]);
@@ -1115,6 +1116,20 @@ DSA_DEV void scan_output(const DeltaArgs& a, const ScanPlace& at, unsigned char*
   }
 }
 
+// Sequence b, head hl of the pass, value columns from dvc on.
+DSA_DEV ScanPlace scan_place(const DeltaArgs& a, int b, int hl, int dvc) {
+  ScanPlace at;
+  at.h = a.head0 + hl;
+  at.hk = at.h / (a.hv / a.hk);
+  at.first = __ldg(a.q_offsets + b);
+  at.len = (int)(__ldg(a.q_offsets + b + 1) - at.first);
+  at.slot = delta_slot(a, b);
+  at.dvc = dvc;
+  at.items = a.ws + (delta_first_slot(a, b) * a.heads + hl) * (int64_t)kDeltaItemBytes;
+  at.item_step = (int64_t)a.heads * kDeltaItemBytes;
+  return at;
+}
+
 template <int PAIRS>
 __global__ void __launch_bounds__(ScanGeo<PAIRS>::kThreads, 1) delta_scan_kernel(
     const DeltaArgs a, const __grid_constant__ DeltaMaps maps) {
@@ -1124,16 +1139,8 @@ __global__ void __launch_bounds__(ScanGeo<PAIRS>::kThreads, 1) delta_scan_kernel
   const int part = blockIdx.x % Geo::kParts;
   const int hl = (blockIdx.x / Geo::kParts) % a.heads;
   const int b = blockIdx.x / (Geo::kParts * a.heads);
-  ScanPlace at;
-  at.h = a.head0 + hl;
-  at.hk = at.h / (a.hv / a.hk);
-  at.first = __ldg(a.q_offsets + b);
-  at.len = (int)(__ldg(a.q_offsets + b + 1) - at.first);
+  const ScanPlace at = scan_place(a, b, hl, part * PAIRS / 2 * kScanNV);
   if (at.len < a.min_len) return;
-  at.slot = delta_slot(a, b);
-  at.dvc = part * PAIRS / 2 * kScanNV;
-  at.items = a.ws + (delta_first_slot(a, b) * a.heads + hl) * (int64_t)kDeltaItemBytes;
-  at.item_step = (int64_t)a.heads * kDeltaItemBytes;
   ScanSync* sy = reinterpret_cast<ScanSync*>(smem + Geo::kBars);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {

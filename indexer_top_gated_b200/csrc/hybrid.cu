@@ -7,6 +7,7 @@
 
 #include "dsa.h"
 #include "gated_delta.cuh"
+#include "gated_delta_umma.cuh"
 #include "hybrid.h"
 #include "rope.cuh"
 #include "short_conv.cuh"
@@ -99,6 +100,7 @@ cudaError_t hybrid_allow_smem() {
   };
   cudaError_t e = allow((const void*)delta_prep_kernel<false>, (int)sizeof(PrepSmem));
   e = e ? e : allow((const void*)delta_prep_kernel<true>, (int)sizeof(PrepSmem));
+  e = e ? e : allow((const void*)delta_umma_kernel, kUmmaSmem);
   e = e ? e : allow((const void*)delta_scan_kernel<1>, ScanGeo<1>::kSmem);
   e = e ? e : allow((const void*)delta_scan_kernel<2>, ScanGeo<2>::kSmem);
   return e;
@@ -428,6 +430,8 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   DSA_TRY(make_row_map(&maps.k, k, R->total_q, P->n_k_heads * kDeltaDim, a.k_stride, 64, kDeltaChunk));
   DSA_TRY(make_row_map(&maps.v, v, R->total_q, P->n_v_heads * kDeltaDim, a.v_stride, kScanNV,
                        kDeltaChunk));
+  DSA_TRY(make_row_map(&maps.out, out, R->total_q, P->n_v_heads * kDeltaDim,
+                       (int64_t)P->n_v_heads * kDeltaDim, 32, kDeltaChunk));
   bool any_short = true;
   if (R->q_offsets_host) {
     any_short = false;
@@ -438,6 +442,13 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   a.min_len = kDeltaShort + 1;
   a.max_len = INT32_MAX;
   a.ws = static_cast<unsigned char*>(workspace);
+  // A head's scan as one CTA on tcgen05, or as CTAs of 16 or 32 of its 128 columns with mma.sync
+  // (shorter steps, a quarter of the work a CTA): tcgen05 once the heads of the longest sequence's
+  // length that the batch amounts to are more than the GPU holds by four CTAs each (8192 tokens,
+  // mma.sync and tcgen05, the whole call: 36 heads 382 and 487 us, 38 heads 652 and 492 us, 64
+  // heads 708 and 552 us, 128 heads 1369 and 692 us; 8 uneven sequences, 8 heads 452 and 491 us, 10
+  // heads 507 and 505 us, 16 heads 716 and 568 us).  Of the whole call, not of a pass, so that the workspace does not change results.
+  const bool umma = (int64_t)R->total_q * a.hv * 4 > (int64_t)R->max_q_len * dev.num_sms;
   for (int h0 = 0; h0 < a.hv; h0 += (int)pass) {
     a.head0 = h0;
     a.heads = (int)std::min<int64_t>(pass, a.hv - h0);
@@ -453,13 +464,18 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
     else
       delta_prep_kernel<false><<<ctas, kPrepThreads, sizeof(PrepSmem), st>>>(a, maps);
     DSA_TRY(launched("delta_prep_kernel"));
-    // 16 value columns a CTA while those CTAs fit the GPU at once: the schedulers of an SM then
-    // carry one warp each (4096 tokens, 16 and 32 columns: 8 heads 148 and 179 us, 18 heads 159
-    // and 188 us, 20 heads 264 and 194 us)
-    if ((int64_t)a.batch * a.heads * ScanGeo<1>::kParts <= dev.num_sms)
+    // (Without tcgen05:) 16 value columns a CTA while those CTAs fit the GPU at once: the schedulers
+    // of an SM then carry one warp each (4096 tokens, 16 and 32 columns: 8 heads 148 and 179 us, 18
+    // heads 159 and 188 us, 20 heads 264 and 194 us)
+    if (umma) {
+      const int64_t ctas = (int64_t)a.batch * a.heads;
+      delta_umma_kernel<<<(unsigned)ctas, kUmmaThreads, kUmmaSmem, st>>>(a, maps);
+      DSA_TRY(launched("delta_umma_kernel"));
+    } else if ((int64_t)a.batch * a.heads * ScanGeo<1>::kParts <= dev.num_sms) {
       DSA_TRY(launch_scan<1>(a, maps, st));
-    else
+    } else {
       DSA_TRY(launch_scan<2>(a, maps, st));
+    }
   }
   return DSA_OK;
 }

@@ -411,59 +411,65 @@ def test_delta_recurrent(lens, norm, heads):
 
 @pytest.mark.parametrize("lens", [[25], [63, 64, 65], [128, 1, 129, 0, 24, 200], [700]])
 @pytest.mark.parametrize("norm", [True, False])
-@pytest.mark.parametrize("heads", [(1, 1), (2, 6)])
+@pytest.mark.parametrize("heads", [(1, 1), (2, 6), (20, 40)])  # 40: a CTA takes a whole head
 def test_delta_chunked(lens, norm, heads):
     d = _Delta(lens, *heads, norm=norm)
     d.check(*d.call())
 
 
+@pytest.mark.parametrize("hv", [2, 40])
 @pytest.mark.parametrize("rate", [0.0, 1e-4, 3.0, 40.0])
-def test_delta_decays(rate):
-    d = _Delta([300, 9], 1, 2, rate=rate)
+def test_delta_decays(rate, hv):
+    d = _Delta([300, 9], 1, hv, rate=rate)
     d.check(*d.call())
 
 
+@pytest.mark.parametrize("hv", [2, 40])
 @pytest.mark.parametrize("beta", [0.0, 1.0])
-def test_delta_write_strengths(beta):
+def test_delta_write_strengths(beta, hv):
     n = 150
-    d = _Delta([n], 1, 2, beta=torch.full((n, 2), beta))
+    d = _Delta([n], 1, hv, beta=torch.full((n, hv), beta))
     d.check(*d.call())
 
 
-def test_delta_decay_to_nothing():
+@pytest.mark.parametrize("hv", [2, 40])
+def test_delta_decay_to_nothing(hv):
     """g = -inf forgets the state; tokens behind it are as if it were the first."""
     n = 200
-    g = torch.full((n, 2), -0.05)
+    g = torch.full((n, hv), -0.05)
     for t in (0, 1, 40, 63, 64, 130):
         g[t, 0] = -math.inf
     g[100:, 1] = -1e30
-    d = _Delta([n], 1, 2, g=g)
+    d = _Delta([n], 1, hv, g=g)
     d.check(*d.call())
-    d = _Delta([7, 3], 1, 2, g=g[:10])
+    d = _Delta([7, 3], 1, hv, g=g[:10])
     d.check(*d.call())
 
 
-def test_delta_equal_keys():
+@pytest.mark.parametrize("hv", [1, 40])
+def test_delta_equal_keys(hv):
     """All keys of a chunk the same: the inverse's entries stay bounded by beta."""
-    d = _Delta([130], 1, 1, rate=0.01)
+    d = _Delta([130], 1, hv, rate=0.01)
     d.k.copy_(d.k[:1].expand_as(d.k).clone())
     d.check(*d.call())
 
 
-def test_delta_many_heads_take_wide_parts():
-    """Sequences times heads beyond the narrow parts' range, uneven lengths."""
-    d = _Delta([70, 25, 129, 90], 4, 24)
+@pytest.mark.parametrize("lens,hk,hv", [([70, 25, 129, 90], 4, 24), ([70, 25, 129, 90], 4, 8), ([200], 8, 32)])
+def test_delta_many_heads_take_wide_parts(lens, hk, hv):
+    """Sequences times heads beyond the narrow parts' range, uneven lengths, and whole heads."""
+    d = _Delta(lens, hk, hv)
     out, st = d.call()
     d.check(out, st)
-    # a head at a time the narrow ones are taken: the same bits
+    # a head at a time, where there are parts the narrow ones are taken: the same bits
     o, s = d.call(ws_bytes=dsa.dsa_gated_delta_workspace_size(d.shape, d.rg)[0])
     assert torch.equal(o, out) and torch.equal(s, st)
 
 
+@pytest.mark.parametrize("hv", [2, 40])
 @pytest.mark.parametrize("lens", [[70, 65], [65, 3, 70]])
-def test_delta_sequences_do_not_touch_one_another(lens):
+def test_delta_sequences_do_not_touch_one_another(lens, hv):
     """NaN and infinities in one sequence leave the others, whose last chunks end beside it, alone."""
-    d = _Delta(lens, 1, 2)
+    d = _Delta(lens, 1, hv)
     want = d.call()
     a, b = lens[0], lens[0] + lens[1]
     for x, bad in ((d.q, math.nan), (d.k, math.inf), (d.v, math.nan), (d.g, math.nan), (d.beta, math.inf)):
@@ -489,8 +495,9 @@ def test_delta_scale_and_few_heads_of_many():
         assert torch.equal(again, out) and torch.equal(st2, st)
 
 
-def test_delta_no_state_no_index_and_padding():
-    d = _Delta([90, 1, 20], extra_rows=70)
+@pytest.mark.parametrize("hv", [4, 40])
+def test_delta_no_state_no_index_and_padding(hv):
+    d = _Delta([90, 1, 20], hv=hv, extra_rows=70)
     out, st = d.call(state_in=None)
     d.check(out, st, zero=True)
     d.index = torch.arange(3, dtype=torch.int32, device="cuda")
@@ -498,14 +505,16 @@ def test_delta_no_state_no_index_and_padding():
     d.check(out, st)
 
 
-def test_delta_slots_outside_are_not_kept():
-    d = _Delta([70, 1, 80, 2])
+@pytest.mark.parametrize("hv", [4, 40])
+def test_delta_slots_outside_are_not_kept(hv):
+    d = _Delta([70, 1, 80, 2], hv=hv)
     d.index[0], d.index[1] = -1, d.slots
     d.check(*d.call())
 
 
-def test_delta_state_in_place():
-    d = _Delta([100, 3, 0, 64])
+@pytest.mark.parametrize("hv", [4, 40])
+def test_delta_state_in_place(hv):
+    d = _Delta([100, 3, 0, 64], hv=hv)
     out, st = d.call()
     state = d.state.clone()
     out2, _ = d.call(state_in=state, state_out=state)
@@ -544,9 +553,10 @@ def test_delta_results_do_not_depend_on_the_workspace_or_the_batch():
     assert torch.equal(stx[int(d.index[1])], st[int(d.index[1])])
 
 
-def test_delta_prefill_then_decode_is_the_whole_sequence():
+@pytest.mark.parametrize("hv", [4, 40])
+def test_delta_prefill_then_decode_is_the_whole_sequence(hv):
     n, steps = 150, 5
-    d = _Delta([n + steps], 2, 4, slots=3)
+    d = _Delta([n + steps], 2, hv, slots=3)
     ref, tol, states = d.ref()
     off = _offsets([n])
     rg = dsa.ragged(off, off, [n], [n])
@@ -554,7 +564,7 @@ def test_delta_prefill_then_decode_is_the_whole_sequence():
     cut = lambda x, a, b: x[a:b].contiguous()  # noqa: E731
     outs = []
     for a, b in [(0, n)] + [(n + i, n + i + 1) for i in range(steps)]:
-        out = torch.empty(b - a, 4, 128, dtype=BF16, device="cuda")
+        out = torch.empty(b - a, hv, 128, dtype=BF16, device="cuda")
         args = [cut(x, a, b) for x in (d.q, d.k, d.v, d.g, d.beta)] + [out]
         kw = dict(state_in=state, state_out=state, state_index=d.index)
         if b - a > 1:
@@ -569,14 +579,15 @@ def test_delta_prefill_then_decode_is_the_whole_sequence():
     assert (state[s].double().cpu() - states[s]).norm() <= 1e-5 * states[s].norm()
 
 
-def test_delta_captured_replays_on_another_stream():
+@pytest.mark.parametrize("hv", [4, 40])
+def test_delta_captured_replays_on_another_stream(hv):
     """A captured call replayed with new inputs, and two calls at once on two streams."""
-    d, e = _Delta([130, 1, 40], 2, 4, seed=1), _Delta([130, 1, 40], 2, 4, seed=9)
+    d, e = _Delta([130, 1, 40], 2, hv, seed=1), _Delta([130, 1, 40], 2, hv, seed=9)
     want_d, want_e = d.call(), e.call()
     size = dsa.dsa_gated_delta_workspace_size(d.shape, d.rg)[1]
     ws = torch.empty(size, dtype=torch.uint8, device="cuda")
     out, st = torch.full_like(want_d[0], 7.0), torch.full_like(want_d[1], 7.0)
-    t = _Delta([130, 1, 40], 2, 4, seed=1)
+    t = _Delta([130, 1, 40], 2, hv, seed=1)
     run = lambda: dsa.dsa_gated_delta_prefill(t.shape, t.rg, t.q, t.k, t.v, t.g, t.beta, out, state_in=t.state,  # noqa: E731
                                               state_out=st, state_index=t.index, workspace=ws)
     side = torch.cuda.Stream()
@@ -607,6 +618,28 @@ def test_delta_captured_replays_on_another_stream():
     torch.cuda.synchronize()
     for (o, so, _), want in zip(got, (want_d, want_e)):
         assert torch.equal(o, want[0]) and torch.equal(so, want[1])
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_delta_whole_heads_alone_and_together(rows):
+    """More heads and sequences than SMs, so that CTAs follow one another: each sequence's results
+    are those of a batch with fewer, and a second call's the first's."""
+    lens = [130, 70, 64, 90, 33, 200][:2 * rows]
+    d = _Delta(lens, 4, 96)
+    out, st = d.call()
+    again, st2 = d.call()
+    assert torch.equal(out, again) and torch.equal(st, st2)
+    few = _Delta(lens, 4, 96)  # one head's share of the heads apart: 24 of 96, the same kernel
+    for h in (0, 24):
+        sel = lambda x: x[:, h:h + 48].contiguous()  # noqa: E731
+        hk = slice(h // 24, h // 24 + 2)
+        o = torch.empty(out.shape[0], 48, 128, dtype=BF16, device="cuda")
+        so = torch.full((d.slots, 48, 128, 128), 7.0, device="cuda")
+        shape = dsa.DeltaShape(2, 48, qk_norm=True, norm_eps=1e-6)
+        ws = torch.empty(dsa.dsa_gated_delta_workspace_size(shape, d.rg)[1], dtype=torch.uint8, device="cuda")
+        dsa.dsa_gated_delta_prefill(shape, d.rg, few.q[:, hk], few.k[:, hk], sel(few.v), sel(few.g), sel(few.beta), o,
+                                    state_in=sel(few.state), state_out=so, state_index=d.index, workspace=ws)
+        assert torch.equal(o, out[:, h:h + 48]) and torch.equal(so, st[:, h:h + 48])
 
 
 def test_delta_decode_large_slots():
