@@ -16,12 +16,12 @@
 // The chain R -> X -> U -> U' -> S bounds it: each operand is released in quarters, whose products
 // run while the next is rounded.  QS and the output are other warps' work, under the chain.
 //
-// Measured: 3.0 us a chunk alone and 3.3 us with every SM busy (4096 tokens x 148 heads: 211 us).
-// Of about 5500 cycles a chunk the tensor pipe has 3400: 24 products of 64 x 64 for U at 38 cycles
-// a K step, S K^T and S Q^T at 45, U' K at 67; the rest is rounding (about 700 cycles for X and for
-// U', bound by the integer pipe that splits values) and hand-overs (250 cycles each).  Loops are
-// kept rolled where registers allow: unrolled, with S in registers, a chunk took as long alone and
-// 4.7 us with every SM busy, waiting for instructions.
+// Measured: 2.9 us a chunk alone and 3.1 us with every SM busy (4096 tokens x 148 heads: 200 us).
+// Of about 5000 cycles a chunk the tensor pipe has 3400: 24 K steps of U at 38 cycles, 16 of R and
+// of QS each at 45, 12 of U' K at 67; the rest is rounding (about 700 cycles for X and for U', bound
+// by the integer pipe that splits values) and hand-overs (250 cycles each).  The code's size counts:
+// unrolled, with S in registers, a chunk took as long alone and 4.7 us with every SM busy, waiting
+// for instructions.  So loops are rolled, X and U' share one, and waits are short.
 #pragma once
 
 #include "gated_delta.cuh"
@@ -51,11 +51,11 @@ constexpr uint32_t kTmCols = 512;
 struct UmmaSync {
   uint64_t full[2], tail;
   uint64_t r_done, q_done, u_done, s_done, o_done;  // products complete
-  uint64_t s_ready[4], x_ready[4], u_ready[4];      // quarters of an operand written
+  uint64_t s_ready[4], x_ready[2][4];               // quarters of S's pieces, and X's or U''s
   uint64_t p_ready, q_free;                         // U's pieces and QS b written; O read
   uint64_t drain;                                   // after a wait that ran out
   uint32_t tmem;
-  int abort;
+  volatile int abort;
 };
 static_assert(sizeof(UmmaSync) <= 256, "");
 
@@ -217,8 +217,21 @@ DSA_DEV void umma_release(uint64_t& bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
 }
+// A bounded wait like mbar_wait_bounded in fewer instructions (there are eighteen of them; reading
+// the clock costs 2 % of the scan): it gives up after as many polls as take 0.1 s or more.
+constexpr uint32_t kUmmaPolls = 1u << 22;
+DSA_DEV void umma_wait_smem(const DeltaArgs& a, UmmaSync* sy, uint64_t& bar, uint32_t parity) {
+  for (uint32_t it = 1; !mbar_try_wait(smem_u32(&bar), parity); ++it) {
+    if (it & 63) continue;
+    if (sy->abort) break;
+    if (it == kUmmaPolls) {
+      sy->abort = 1;
+      atomicExch(a.status, kDevTimeout);
+    }
+  }
+}
 DSA_DEV void umma_wait(const DeltaArgs& a, UmmaSync* sy, uint64_t& bar, uint32_t parity) {
-  mbar_wait_bounded(smem_u32(&bar), parity, a.status, &sy->abort);
+  umma_wait_smem(a, sy, bar, parity);
   tc_fence_after();
 }
 
@@ -229,7 +242,7 @@ DSA_DEV void umma_load(const DeltaArgs& a, const DeltaMaps& maps, const ScanPlac
 #pragma unroll 1
   for (int c = 0; c * kDeltaChunk < at.len; ++c) {
     if (c >= 2)  // chunk c - 2's products are complete and its scalars and V read
-      mbar_wait_bounded(smem_u32(&sy->q_free), c & 1, a.status, &sy->abort);
+      umma_wait_smem(a, sy, sy->q_free, c & 1);
     const int valid = at.len - c * kDeltaChunk;
     const bool part = valid < kDeltaChunk;
     const uint32_t full = smem_u32(&sy->full[c & 1]);
@@ -255,7 +268,7 @@ DSA_DEV void umma_load(const DeltaArgs& a, const DeltaMaps& maps, const ScanPlac
     }
     __syncwarp();
     if (part) {  // the last chunk: the rows behind the sequence's end become zeros first
-      mbar_wait_bounded(bar, 0, a.status, &sy->abort);
+      umma_wait_smem(a, sy, sy->tail, 0);
       for (int i = 0; i < 4; ++i) {
         delta_zero_rows(to + i * (kDeltaTile / 2), 128, valid, lane, 32);
         delta_zero_rows(to + kUmmaV + i * kUmmaVTile, 64, valid, lane, 32);
@@ -290,7 +303,7 @@ DSA_DEV void umma_issue(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
     };
     umma_wait(a, sy, sy->full[par], c >> 1 & 1);
     if (c) umma_wait(a, sy, sy->o_done, 1 - par);
-#pragma unroll 1
+#pragma unroll
     for (int h = 0; h < 4; ++h) {
       umma_wait(a, sy, sy->s_ready[h], par);
       times_s(kTmR, 0, h);
@@ -300,9 +313,9 @@ DSA_DEV void umma_issue(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
 #pragma unroll 1
     for (int h = 0; h < 4; ++h) times_s(kTmQ, kDeltaTile, h);
     umma_commit(smem_u32(&sy->q_done));
-#pragma unroll 1
+#pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-      umma_wait(a, sy, sy->x_ready[kt], par);
+      umma_wait(a, sy, sy->x_ready[0][kt], par);
 #pragma unroll
       for (int px = 0; px < 3; ++px)
 #pragma unroll
@@ -311,9 +324,9 @@ DSA_DEV void umma_issue(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
                        kt + px + pt != 0);
     }
     umma_commit(smem_u32(&sy->u_done));
-#pragma unroll 1
+#pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-      umma_wait(a, sy, sy->u_ready[kt], par);
+      umma_wait(a, sy, sy->x_ready[1][kt], par);
 #pragma unroll
       for (int p = 0; p < 3; ++p)
         umma_bf16_ta(kTmSp, kTmX + p * 32 + kt * 8, dkt + kt * 2048 / 16, kN128Mn, kt + p != 0);
@@ -393,41 +406,36 @@ DSA_DEV void umma_round(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
       }
       tmem_wait_st();
     };
-    // The accumulators are read whole before a quarter is released: its products write over them.
-    float x[4][2][4];
     umma_wait(a, sy, sy->full[par], c >> 1 & 1);
-    {  // X = V - R diag(a)
+    // The accumulators are read whole before a quarter is released: its products write over them.
+#pragma unroll 1
+    for (int p = 0; p < 2; ++p) {  // X = V - R diag(a), then U' = U diag(t)
+      float x[4][2][4];
       uint32_t fv[4][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        ldmatrix_x4_trans(v + swz64(t * 16 + part * 8 + mr, mi), fv[t]);
-      umma_wait(a, sy, sy->r_done, par);
+      for (int t = 0; t < 4; ++t) {
+        if (p == 0) {
+          ldmatrix_x4_trans(v + swz64(t * 16 + part * 8 + mr, mi), fv[t]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) fv[t][e] = 0;
+        }
+      }
+      umma_wait(a, sy, p ? sy->u_done : sy->r_done, par);
       tmem_load_quarters(tm + kTmR + part * 8, x);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const float2 av = *reinterpret_cast<const float2*>(scal + t * 16);
+        const float2 m = *reinterpret_cast<const float2*>(scal + p * 64 + t * 16);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           fma_f32x2(x[t][e >> 1][(e & 1) * 2], x[t][e >> 1][(e & 1) * 2 + 1],
-                    make_float2(-av.x, -av.y), make_float2(bf16_lo(fv[t][e]), bf16_hi(fv[t][e])));
+                    p ? m : make_float2(-m.x, -m.y),
+                    make_float2(bf16_lo(fv[t][e]), bf16_hi(fv[t][e])));
         put_x(x[t], t);
-        umma_release(sy->x_ready[t]);
+        umma_release(sy->x_ready[p][t]);
       }
     }
     const float decay = reinterpret_cast<const float*>(stage + kUmmaScal)[192];
-    {  // U' = U diag(t)
-      umma_wait(a, sy, sy->u_done, par);
-      tmem_load_quarters(tm + kTmR + part * 8, x);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float2 tv = *reinterpret_cast<const float2*>(scal + 64 + t * 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mul_f32x2(x[t][e >> 1][(e & 1) * 2], x[t][e >> 1][(e & 1) * 2 + 1], tv);
-        put_x(x[t], t);
-        umma_release(sy->u_ready[t]);
-      }
-    }
     umma_wait(a, sy, sy->s_done, par);
 #pragma unroll 1
     for (int h = 0; h < 4; ++h) {  // S = e^(G_C) S + U' K
@@ -485,8 +493,8 @@ DSA_DEV void umma_output(const DeltaArgs& a, const DeltaMaps& maps, const ScanPl
       tmem_st_tiles(tm + kTmQ + t * 16, x[0]);
       tmem_st_tiles(tm + kTmQ + t * 16 + kHalfLanes, x[1]);
     }
-    umma_wait(a, sy, sy->u_done, par);
-    umma_wait(a, sy, sy->u_ready[0], par);  // the chain has read U, whose place the second piece takes
+    // U is there, and the chain has read it: the second piece takes its place
+    umma_wait(a, sy, sy->x_ready[1][0], par);
 #pragma unroll 1
     for (int t = 0; t < 4; ++t) {
       tmem_load16(tm + kTmR + t * 16, x);
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1) delta_umma_kernel(
                         &sy->u_done, &sy->s_done, &sy->o_done, &sy->drain})
       mbar_init(smem_u32(b), 1);
     for (int h = 0; h < 4; ++h)
-      for (uint64_t* b : {&sy->s_ready[h], &sy->x_ready[h], &sy->u_ready[h]})
+      for (uint64_t* b : {&sy->s_ready[h], &sy->x_ready[0][h], &sy->x_ready[1][h]})
         mbar_init(smem_u32(b), kUmmaChain);
     for (uint64_t* b : {&sy->p_ready, &sy->q_free}) mbar_init(smem_u32(b), kUmmaOutWarps);
     sy->abort = 0;

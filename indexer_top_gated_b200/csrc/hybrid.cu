@@ -445,9 +445,9 @@ dsa_status dsa_gated_delta_prefill(const dsa_delta_params* P, const dsa_ragged* 
   // A head's scan as one CTA on tcgen05, or as CTAs of 16 or 32 of its 128 columns with mma.sync
   // (shorter steps, a quarter of the work a CTA): tcgen05 once the heads of the longest sequence's
   // length that the batch amounts to are more than the GPU holds by four CTAs each (8192 tokens,
-  // mma.sync and tcgen05, the whole call: 36 heads 382 and 487 us, 38 heads 652 and 492 us, 64
-  // heads 708 and 552 us, 128 heads 1369 and 692 us; 8 uneven sequences, 8 heads 452 and 491 us, 10
-  // heads 507 and 505 us, 16 heads 716 and 568 us).  Of the whole call, not of a pass, so that the workspace does not change results.
+  // mma.sync and tcgen05, the whole call: 36 heads 380 and 456 us, 38 heads 641 and 459 us, 64
+  // heads 702 and 515 us, 128 heads 1361 and 656 us; 8 uneven sequences, 8 heads 448 and 456 us, 10
+  // heads 504 and 475 us, 16 heads 713 and 531 us).  Of the whole call, not of a pass, so that the workspace does not change results.
   const bool umma = (int64_t)R->total_q * a.hv * 4 > (int64_t)R->max_q_len * dev.num_sms;
   for (int h0 = 0; h0 < a.hv; h0 += (int)pass) {
     a.head0 = h0;
