@@ -543,9 +543,8 @@ typedef struct {
  * bf16 pieces that keep the state within about 1e-6 of itself).  A sequence's results do not depend
  * on the workspace's size, and on the rest of the batch only in the last bits, through the choice
  * of the kernel: one for batches whose heads fill the GPU (total_q * n_v_heads against max_q_len),
- * one for fewer.  A NaN or an infinity in a token's
- * inputs stays in its sequence and value heads, but within its chunk of 64 it may reach the outputs
- * of tokens before it.
+ * one for fewer.  A NaN or an infinity in a token's inputs stays in its sequence and value heads,
+ * but within its chunk of 64 it may reach the outputs of tokens before it.
  * dsa_gated_delta_decode is for at most one token per sequence (max_q_len <= 1) and takes no
  * workspace.
  *   workspace   device, 256-byte aligned, ws_bytes >= the minimum of
