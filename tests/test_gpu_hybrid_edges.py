@@ -1,0 +1,68 @@
+"""GPU checks of the operators around the layer where they can go wrong besides sizes: extreme values,
+infinities and NaN, descriptors of which only the documented fields are filled, batches of single
+tokens, captured calls and streams.  Plain 64-bit computations are the reference."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+dsa = None
+BF16 = torch.bfloat16
+U = 2.0 ** -8  # half a step of bf16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    global dsa
+    import indexer_top_gated_b200 as m
+    dsa = m
+    torch.cuda.init()
+    yield
+    assert dsa.dsa_device_status(clear=True) == 0
+
+
+def _offsets(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def _randn(seed, *shape, scale=1.0, dtype=BF16):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=gen) * scale).to(dtype).cuda()
+
+
+# ---------------------------------------------------------------- short convolution
+
+LOWEST = float(torch.finfo(BF16).min)
+EXTREMES = [LOWEST, -1e30, -1e20, -1e17, -1e6, -1000.0, -128.0, -104.0, -96.0, -89.0, -88.0, -87.0, -80.0, -64.0,
+            -50.0, -41.0, -40.0, -20.0, -1.0, -1e-30, 0.0, 1e-30, 1.0, 20.0, 100.0, 1e20, -LOWEST, float("inf"),
+            float("-inf"), float("nan")]
+
+
+@pytest.mark.parametrize("lens", [[1], [9], [30000]])
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_conv_activation_of_extreme_values(lens, width):
+    """y / (1 + e^-y) of every pair of extreme values in neighbouring channels (they share registers).
+    The last tap is 1 and the others 0, so y is x itself.  Tolerance: the output's rounding, 2^-15 of
+    the value (an exponent of up to 127 in fp32 is off by 127 half steps, twice that with its factor
+    log2 e) and 2^-119, above 88 * 2^-126, for what a reciprocal flushed to zero leaves out."""
+    pairs = torch.tensor([v for a in EXTREMES for b in EXTREMES for v in (a, b)], dtype=BF16)
+    c = len(pairs)
+    n = sum(lens)
+    x = torch.zeros(n, c, dtype=BF16, device="cuda")
+    rows = sorted({0, n // 2, n - 1})  # alone in their windows
+    x[rows] = pairs.cuda()
+    weight = torch.zeros(c, width, dtype=BF16, device="cuda")
+    weight[:, -1] = 1.0
+    out = torch.full_like(x, 7.0)
+    off = _offsets(lens)
+    dsa.dsa_short_conv(dsa.ConvShape(c, width), dsa.ragged(off, off, lens, lens), x, weight, out)
+    y = pairs.double()
+    ref = y / (1 + torch.exp(-y))
+    for r in rows:
+        got = out[r].double().cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), r
+        wild = torch.isnan(ref) | torch.isinf(ref)
+        assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+        over = ((got - ref).abs() > (U + 2.0 ** -15) * ref.abs() + 2.0 ** -119) & ~wild
+        assert not over.any(), (r, [(float(y[i]), float(got[i]), float(ref[i])) for i in torch.nonzero(over)[:4, 0]])
