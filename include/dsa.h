@@ -505,9 +505,9 @@ typedef struct {
  *               Slots of one call are distinct; a sequence whose slot is outside 0 ..
  *               n_states-1 starts from zeros and its state is not kept.
  * Sums are fp32, the output is rounded once.  Only batch, q_offsets and total_q of dsa_ragged
- * are read.  Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps
- * neither x, the weights nor a state; state_out is state_in or does not overlap it, nor anything
- * else.
+ * decide the results; a max_q_len of 1 selects the form for single tokens, for speed alone.
+ * Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps neither x, the
+ * weights nor a state; state_out is state_in or does not overlap it, nor anything else.
  */
 dsa_status dsa_short_conv(const dsa_conv_params* params, const dsa_ragged* ragged, const void* x,
                           const void* weight, const void* bias, const void* state_in,

@@ -48,10 +48,13 @@ bool overlap(const Span& a, const Span& b) {
 }
 
 dsa_status check_rows(const dsa_ragged* R) {
-  if (!R || R->batch < 1 || !R->q_offsets || R->max_q_len < 0 || R->total_q < 0)
-    return DSA_ERR_INVALID_ARG;
+  if (!R || R->batch < 1 || !R->q_offsets || R->total_q < 0) return DSA_ERR_INVALID_ARG;
   if (R->total_q > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
+}
+dsa_status check_lens(const dsa_ragged* R) {
+  DSA_TRY(check_rows(R));
+  return R->max_q_len < 0 ? DSA_ERR_INVALID_ARG : DSA_OK;
 }
 
 // The row stride to use: `stride`, or `width` when it is 0; -1 when invalid.
@@ -115,7 +118,7 @@ extern "C" {
 dsa_status dsa_rope_append(const dsa_params* P, const dsa_ragged* R, const dsa_rope_params* O,
                            const dsa_rope_buffers* B, const int32_t* positions,
                            int32_t* err_count, void* stream) {
-  DSA_TRY(check_rows(R));
+  DSA_TRY(check_lens(R));
   if (!P || !O || !B || !R->kv_offsets || R->total_kv < 0) return DSA_ERR_INVALID_ARG;
   if (R->total_kv > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   const bool att = B->q || B->k || B->v, idx = B->q_idx || B->k_idx;
@@ -237,7 +240,8 @@ dsa_status launch_conv(const ConvArgs& a, const dsa_ragged* R, int sms, cudaStre
   // runs of 8 and of 48 rows: 300 rows 6.7 and 13.0 us, 1500 rows 16.4 and 14.9 us, 8000 rows 91
   // and 65 us)
   const bool wide = R->total_q / kConvRun * groups * 2 >= 3 * (int64_t)sms;
-  const bool single = R->max_q_len <= 1;
+  // (max_q_len may be unset: either form takes sequences of any length)
+  const bool single = R->max_q_len == 1;
   const int64_t runs = single ? R->batch : R->total_q / (wide ? kConvRun : 8) + R->batch;
   const unsigned y = (unsigned)std::min<int64_t>(runs, 32768);
   const dim3 grid((unsigned)groups, y, (unsigned)((runs + y - 1) / y));
@@ -309,7 +313,7 @@ namespace {
 constexpr int kDeltaShort = 24;
 
 dsa_status check_delta(const dsa_delta_params* P, const dsa_ragged* R) {
-  DSA_TRY(check_rows(R));
+  DSA_TRY(check_lens(R));
   if (!P) return DSA_ERR_INVALID_ARG;
   if (P->head_dim != kDeltaDim) return DSA_ERR_UNSUPPORTED;
   if (P->n_k_heads < 1 || P->n_v_heads < 1 || P->n_v_heads % P->n_k_heads != 0)

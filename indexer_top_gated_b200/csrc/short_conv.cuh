@@ -54,13 +54,14 @@ DSA_DEV void conv_unpack(uint4 x, uint64_t (&f)[4]) {
 
 // Grid: x = channel groups, y = runs.  Run k of sequence b is run q_offsets[b] / RUN + b + k
 // (runs start at the sequence's first row, so only a sequence's first run reads its state, and
-// the threads that read it are those that write the new one: in place is safe).
+// the threads that read it are those that write the new one: in place is safe).  RUN == 1, for
+// single tokens: run b is sequence b, all of it.
 template <int W, int RUN>
 __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs a) {
   const int c0 = (blockIdx.x * kConvThreads + threadIdx.x) * 8;
   const int64_t run = (int64_t)blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
   int b = 0;
-  if (RUN == 1) {  // single tokens: run b is sequence b
+  if (RUN == 1) {
     if (run >= a.batch) return;
     b = (int)run;
   } else {
@@ -133,12 +134,13 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
   for (int j = 0; j < H; ++j) conv_unpack(hist[j], win[j]);
 
   const int64_t t0 = k * RUN;
-  const int rows = (int)(n - t0 < RUN ? n - t0 : RUN);
+  const int rows = (int)(RUN == 1 || n - t0 < RUN ? n - t0 : RUN);
   __nv_bfloat16* out = a.out + (first + t0) * a.out_stride + c0;
   x += t0 * a.x_stride;
   // A ring of rows in shared memory keeps kGroup of them in flight without holding registers.  A
   // thread reads back only what it copied itself: no barrier.  A group of rows turns ring and
-  // window a whole number of times, so both are indexed by constants.
+  // window a whole number of times, so both are indexed by constants (a group of one row turns the
+  // window itself).
   constexpr int kGroup = RUN == 1 ? 1 : H == 3 ? 6 : 8;
   __shared__ uint4 ring[kGroup][kConvThreads];
   const uint4* mine = &ring[0][threadIdx.x];
@@ -184,6 +186,15 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
         __stcs(reinterpret_cast<uint4*>(out),
                make_uint4(packed[0], packed[1], packed[2], packed[3]));
       out += out_step;
+    }
+    if (kGroup == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t newest = win[0][i];
+#pragma unroll
+        for (int j = 0; j + 1 < H; ++j) win[j][i] = win[j + 1][i];
+        win[H - 1][i] = newest;
+      }
     }
   }
 }

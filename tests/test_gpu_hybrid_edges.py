@@ -66,3 +66,20 @@ def test_conv_activation_of_extreme_values(lens, width):
         assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
         over = ((got - ref).abs() > (U + 2.0 ** -15) * ref.abs() + 2.0 ** -119) & ~wild
         assert not over.any(), (r, [(float(y[i]), float(got[i]), float(ref[i])) for i in torch.nonzero(over)[:4, 0]])
+
+
+@pytest.mark.parametrize("max_q_len", [0, 1, -7, 1 << 30])
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_conv_results_do_not_depend_on_max_q_len(max_q_len, width):
+    """Of the descriptor only batch, q_offsets and total_q are filled; max_q_len is whatever it is."""
+    lens, c = [70, 0, 1, 33, 2], 264
+    n, slots = sum(lens), len(lens)
+    x, weight, state = _randn(1, n, c), _randn(2, c, width), _randn(3, slots, width - 1, c)
+    off = _offsets(lens)
+    conv = dsa.ConvShape(c, width)
+    want, want_state = torch.empty_like(x), torch.empty_like(state)
+    dsa.dsa_short_conv(conv, dsa.ragged(off, off, lens, lens), x, weight, want, state_in=state, state_out=want_state)
+    rg = dsa.Ragged(slots, off.data_ptr(), None, max_q_len, 0, n, 0)
+    out, st = torch.full_like(x, 7.0), torch.full_like(state, 7.0)
+    dsa.dsa_short_conv(conv, rg, x, weight, out, state_in=state, state_out=st)
+    assert torch.equal(out, want) and torch.equal(st, want_state)
