@@ -5,7 +5,7 @@
 // Bound: HBM, closely followed by instruction issue (an exponential and a reciprocal for each
 // activation).  A thread walks a run of rows of 8 channels (48, in small batches 8, 1 for single
 // tokens) with the window in registers, so a row is read once (and W - 1 rows again where a run
-// begins).  Measured: 32768 rows x 8192 channels 181 us, 5.9 TB/s.
+// begins).  Measured: 32768 rows x 8192 channels 172 us, 6.2 TB/s.
 #pragma once
 
 #include "common.cuh"
@@ -56,8 +56,10 @@ DSA_DEV void conv_unpack(uint4 x, uint64_t (&f)[4]) {
 // (runs start at the sequence's first row, so only a sequence's first run reads its state, and
 // the threads that read it are those that write the new one: in place is safe).  RUN == 1, for
 // single tokens: run b is sequence b, all of it.
+// Four CTAs an SM, said to the compiler: left to itself it spilled with three taps for the sake of
+// a sixth CTA (14000 rows x 5128 channels 55.4 us, so 51.5; the other widths as fast or 1 % faster).
 template <int W, int RUN>
-__global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const ConvArgs a) {
   const int c0 = (blockIdx.x * kConvThreads + threadIdx.x) * 8;
   const int64_t run = (int64_t)blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
   int b = 0;
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
         if (a.silu) {
           // y / (1 + e^-y).  Where 1 + e^-y passes 2^126 (y below -87) its reciprocal is 0.  (One
           // reciprocal for both by their product needs bounded exponents, which is wrong for large
-          // -y, and took two instructions more: 199 us)
+          // -y, and took two instructions more: 199 against 181 us)
           constexpr float kLog2e = 1.44269504f;
           y0 *= rcp_approx(1.f + ex2_approx(-kLog2e * y0));
           y1 *= rcp_approx(1.f + ex2_approx(-kLog2e * y1));
