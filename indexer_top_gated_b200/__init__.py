@@ -443,6 +443,8 @@ def _rows(where, name, t, dtype, shape, device):
         if steps[i] != dense and shape[i] > 1:
             _bad(where, f"{name} has rows that are not dense (strides {steps})")
         dense *= shape[i]
+    if shape[0] > 1 and steps[0] < dense:  # repeated or overlapping (0 would mean packed)
+        _bad(where, f"{name} has rows that are not apart (strides {steps})")
     return t.data_ptr(), steps[0]
 
 

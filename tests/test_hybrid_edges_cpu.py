@@ -13,3 +13,24 @@ def test_conv_does_not_judge_max_q_len(dsa):  # noqa: F811
         rg = _rg(dsa, max_q_len=max_q_len)
         assert _conv(dsa, rg=rg, width=5) == dsa.DSA_ERR_UNSUPPORTED
         assert _conv(dsa, rg=rg, ptrs=dict(weight=None)) == dsa.DSA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("shape", [(5, 64), (5, 4, 128)])
+def test_binding_refuses_repeated_and_overlapping_rows(dsa, shape):  # noqa: F811
+    """A row stride of 0 means packed rows to the library, so a broadcast tensor must not reach it; nor
+    rows that overlap.  (get_device() of a CPU tensor is -1.)"""
+    import torch
+    row = torch.zeros(1, *shape[1:], dtype=torch.bfloat16)
+    rows = lambda t: dsa._rows("call", "x", t, torch.bfloat16, shape, -1)  # noqa: E731
+    width = row.numel()
+    for bad in (row.expand(shape), torch.zeros(4096, dtype=torch.bfloat16).as_strided(shape, (8, *row.stride()[1:])),
+                row.expand(9, *shape[1:])):
+        with pytest.raises(dsa.DsaError):
+            rows(bad)
+    wide = torch.zeros(5, width + 8, dtype=torch.bfloat16)
+    assert rows(wide[:, :width].view(shape)) == (wide.data_ptr(), width + 8)
+    assert rows(torch.zeros(shape, dtype=torch.bfloat16))[1] == 0
+    # one row or none: there is nothing to repeat
+    one = (1, *shape[1:])
+    assert dsa._rows("call", "x", row.expand(shape)[:1], torch.bfloat16, one, -1) == (row.data_ptr(), 0)
+    assert dsa._rows("call", "x", row.expand(shape), torch.bfloat16, one, -1) == (row.data_ptr(), 0)
