@@ -564,6 +564,20 @@ def _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out, st
     return _delta_params(delta, ns, (sq, sk, sv)), (pq, pk, pv, pg, pb, s0, s1, pi, po)
 
 
+def _workspace(where, workspace, ws_bytes, device):
+    """Address and bytes of a workspace tensor (ws_bytes of it, or all)."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != device:
+        _bad(where, f"workspace on {workspace.device}, not cuda:{device}")
+    if not workspace.is_contiguous():
+        _bad(where, "workspace is not contiguous")
+    held = workspace.numel() * workspace.element_size()
+    if ws_bytes is not None and not 0 <= ws_bytes <= held:
+        _bad(where, f"ws_bytes is {ws_bytes}, the workspace has {held}")
+    return workspace.data_ptr(), held if ws_bytes is None else ws_bytes
+
+
 def dsa_gated_delta_workspace_size(delta: DeltaShape, rg: Ragged):
     p = _delta_params(delta)
     mn, rec = ctypes.c_size_t(0), ctypes.c_size_t(0)
@@ -579,12 +593,9 @@ def dsa_gated_delta_prefill(delta: DeltaShape, rg: Ragged, q, k, v, g, beta, out
     where, device = "dsa_gated_delta_prefill", _device(stream)
     p, args = _delta_args(where, delta, rg, q, k, v, g, beta, out, state_in, state_out,
                           state_index, device)
-    if ws_bytes is None:
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if workspace is not None and workspace.get_device() != device:
-        _bad(where, f"workspace on {workspace.device}, not cuda:{device}")
-    _check(lib.dsa_gated_delta_prefill(ctypes.byref(p), ctypes.byref(rg), *args, _ptr(workspace),
-                                       ws_bytes, _raw_stream(stream, device)), where)
+    _check(lib.dsa_gated_delta_prefill(ctypes.byref(p), ctypes.byref(rg), *args,
+                                       *_workspace(where, workspace, ws_bytes, device),
+                                       _raw_stream(stream, device)), where)
 
 
 def dsa_gated_delta_decode(delta: DeltaShape, rg: Ragged, q, k, v, g, beta, out, state_in=None,

@@ -34,3 +34,16 @@ def test_binding_refuses_repeated_and_overlapping_rows(dsa, shape):  # noqa: F81
     one = (1, *shape[1:])
     assert dsa._rows("call", "x", row.expand(shape)[:1], torch.bfloat16, one, -1) == (row.data_ptr(), 0)
     assert dsa._rows("call", "x", row.expand(shape), torch.bfloat16, one, -1) == (row.data_ptr(), 0)
+
+
+def test_binding_refuses_a_workspace_smaller_than_it_says(dsa):  # noqa: F811
+    import torch
+    ws = torch.zeros(64, dtype=torch.int32)
+    take = lambda t, n=None: dsa._workspace("call", t, n, -1)  # noqa: E731
+    assert take(ws) == (ws.data_ptr(), 256) and take(ws, 100) == (ws.data_ptr(), 100)
+    assert take(None) == (None, 0) and take(None, 64) == (None, 0)
+    for t, n in ((ws[:1].expand(64), None), (ws[::2], None), (ws, 257), (ws, -1)):
+        with pytest.raises(dsa.DsaError):
+            take(t, n)
+    with pytest.raises(dsa.DsaError):
+        dsa._workspace("call", ws, None, 0)
