@@ -90,7 +90,7 @@ dsa_status rope_freqs(const dsa_rope_params* O, int rot, double* f) {
 }
 
 dsa_status check_rot(int rot, int off, int dim) {
-  if (rot < 0 || off < 0 || off + rot > dim) return DSA_ERR_INVALID_ARG;
+  if (rot < 0 || rot > dim || off < 0 || off > dim - rot) return DSA_ERR_INVALID_ARG;
   if (rot % 16 != 0 || off % 8 != 0) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }

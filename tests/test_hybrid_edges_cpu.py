@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from tests.test_hybrid_cpu import _at, _conv, _rg, dsa  # noqa: F401  (a fixture)
+from tests.test_hybrid_cpu import _at, _conv, _rg, _rope, dsa  # noqa: F401  (a fixture)
 
 
 def test_conv_does_not_judge_max_q_len(dsa):  # noqa: F811
@@ -47,3 +47,14 @@ def test_binding_refuses_a_workspace_smaller_than_it_says(dsa):  # noqa: F811
             take(t, n)
     with pytest.raises(dsa.DsaError):
         dsa._workspace("call", ws, None, 0)
+
+
+@pytest.mark.parametrize("kw", [dict(rot_dim=16, rot_offset=(1 << 31) - 8), dict(rot_dim=128, rot_offset=(1 << 31) - 128),
+                                dict(rot_dim=(1 << 31) - 16, rot_offset=(1 << 31) - 8),
+                                dict(idx_rot_dim=64, idx_rot_offset=(1 << 31) - 64)])
+def test_rope_offsets_whose_end_overflows(dsa, kw):  # noqa: F811
+    """offset + dimensions beyond 2^31 is past the head, not negative."""
+    none = {n: None for n, _ in dsa.RopeBuffers._fields_}
+    for buffers in (dict(none, q=_at(0), q_out=_at(5)), dict(none, q_idx=_at(3), q_idx_out=_at(8))):
+        if ("rot_dim" in kw) == (buffers["q"] is not None):
+            assert _rope(dsa, rg=_rg(dsa, total_q=0), buffers=buffers, **kw) == dsa.DSA_ERR_INVALID_ARG
