@@ -407,6 +407,9 @@ DSA_DEV void umma_round(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
       tmem_wait_st();
     };
     umma_wait(a, sy, sy->full[par], c >> 1 & 1);
+    // (read here, not where it is used: after a warp's last release of X or U' nothing keeps the
+    // loader from the stage)
+    const float decay = reinterpret_cast<const float*>(stage + kUmmaScal)[192];
     // The accumulators are read whole before a quarter is released: its products write over them.
 #pragma unroll 1
     for (int p = 0; p < 2; ++p) {  // X = V - R diag(a), then U' = U diag(t)
@@ -435,7 +438,6 @@ DSA_DEV void umma_round(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
         umma_release(sy->x_ready[p][t]);
       }
     }
-    const float decay = reinterpret_cast<const float*>(stage + kUmmaScal)[192];
     umma_wait(a, sy, sy->s_done, par);
 #pragma unroll 1
     for (int h = 0; h < 4; ++h) {  // S = e^(G_C) S + U' K

@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+from tests import test_gpu_hybrid as T
+
 pytestmark = pytest.mark.gpu
 
 dsa = None
@@ -16,7 +18,7 @@ U = 2.0 ** -8  # half a step of bf16
 def _lib():
     global dsa
     import indexer_top_gated_b200 as m
-    dsa = m
+    dsa = T.dsa = m
     torch.cuda.init()
     yield
     assert dsa.dsa_device_status(clear=True) == 0
@@ -83,3 +85,42 @@ def test_conv_results_do_not_depend_on_max_q_len(max_q_len, width):
     out, st = torch.full_like(x, 7.0), torch.full_like(state, 7.0)
     dsa.dsa_short_conv(conv, rg, x, weight, out, state_in=state, state_out=st)
     assert torch.equal(out, want) and torch.equal(st, want_state)
+
+
+# ---------------------------------------------------------------- gated delta rule
+
+def _delta_states(d):
+    """States after token after token, 64 bits, on the GPU: [sequence, Hv, dv, dk]."""
+    n, rep = d.n, d.hv // d.hk
+    k, v = d.k[:n].double(), d.v[:n].double()
+    if d.norm:
+        k = k / torch.sqrt((k * k).sum(-1, keepdim=True) + 1e-6)
+    k = k.repeat_interleave(rep, 1)
+    alpha, beta = torch.exp(d.g[:n].double()), d.beta[:n].double()
+    S = d.state[d.index.long()].double()
+    at = 0
+    for b, m in enumerate(d.lens):
+        s = S[b]
+        for t in range(at, at + m):
+            s *= alpha[t][:, None, None]
+            u = beta[t][:, None] * (v[t] - (s @ k[t][..., None])[..., 0])
+            s += u[..., None] * k[t][:, None, :]
+        at += m
+    return S
+
+
+# few heads; 32 columns a CTA; whole heads (of 40, and of 148: one for each SM)
+@pytest.mark.parametrize("hk,hv,lens", [(1, 2, [1300]), (2, 24, [1300]), (2, 40, [1300]), (4, 148, [1300, 5])])
+def test_delta_decays_of_each_chunk_its_own(hk, hv, lens):
+    """Chunks of 64 whose decays differ by factors from one to the next and to the one after it (which
+    takes its place in shared memory).  A chunk's decay in another's place moves the state by more than
+    a tenth of itself; tolerance 1e-5 of each head's."""
+    d = T._Delta(lens, hk, hv, rate=0.0)
+    n = sum(lens)
+    per_chunk = torch.tensor([0.0, -0.4, -1.2, 0.0, -2.5])[torch.arange(n) // 64 % 5]
+    per_head = torch.linspace(0.5, 1.0, hv)
+    d.g = (per_chunk[:, None] * per_head / 64).cuda().contiguous()
+    _, st = d.call()
+    want = _delta_states(d)
+    off = (st[d.index.long()].double() - want).flatten(2).norm(dim=-1)
+    assert (off <= 1e-5 * want.flatten(2).norm(dim=-1)).all(), float((off / want.flatten(2).norm(dim=-1)).max())
