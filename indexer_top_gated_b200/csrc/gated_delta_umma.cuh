@@ -52,7 +52,10 @@ struct UmmaSync {
   uint64_t full[2], tail;
   uint64_t r_done, q_done, u_done, s_done, o_done;  // products complete
   uint64_t s_ready[4], x_ready[2][4];               // quarters of S's pieces, and X's or U''s
-  uint64_t p_ready, q_free;                         // U's pieces and QS b written; O read
+  uint64_t p_ready;                                 // U's pieces and QS b written
+  // O read: one for each stage, since two chunks are under way when the loader asks for the first
+  // of them, and a barrier waited for by parity may not be two phases ahead
+  uint64_t q_free[2];
   uint64_t drain;                                   // after a wait that ran out
   uint32_t tmem;
   volatile int abort;
@@ -242,7 +245,7 @@ DSA_DEV void umma_load(const DeltaArgs& a, const DeltaMaps& maps, const ScanPlac
 #pragma unroll 1
   for (int c = 0; c * kDeltaChunk < at.len; ++c) {
     if (c >= 2)  // chunk c - 2's products are complete and its scalars and V read
-      umma_wait_smem(a, sy, sy->q_free, c & 1);
+      umma_wait_smem(a, sy, sy->q_free[c & 1], (c >> 1 & 1) ^ 1);
     const int valid = at.len - c * kDeltaChunk;
     const bool part = valid < kDeltaChunk;
     const uint32_t full = smem_u32(&sy->full[c & 1]);
@@ -309,7 +312,7 @@ DSA_DEV void umma_issue(const DeltaArgs& a, const ScanPlace& at, unsigned char* 
       times_s(kTmR, 0, h);
     }
     umma_commit(smem_u32(&sy->r_done));
-    if (c) umma_wait(a, sy, sy->q_free, 1 - par);
+    if (c) umma_wait(a, sy, sy->q_free[1 - par], (c - 1) >> 1 & 1);
 #pragma unroll 1
     for (int h = 0; h < 4; ++h) times_s(kTmQ, kDeltaTile, h);
     umma_commit(smem_u32(&sy->q_done));
@@ -526,7 +529,7 @@ DSA_DEV void umma_output(const DeltaArgs& a, const DeltaMaps& maps, const ScanPl
                           pack_bf16x2(x[h][0], x[h][1]), pack_bf16x2(x[h][2], x[h][3]),
                           pack_bf16x2(x[h][4], x[h][5]), pack_bf16x2(x[h][6], x[h][7]));
     }
-    umma_release(sy->q_free);
+    umma_release(sy->q_free[par]);
     const int row = c * kDeltaChunk, left = at.len - row;
     if (left >= kDeltaChunk) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1) delta_umma_kernel(
     for (int h = 0; h < 4; ++h)
       for (uint64_t* b : {&sy->s_ready[h], &sy->x_ready[0][h], &sy->x_ready[1][h]})
         mbar_init(smem_u32(b), kUmmaChain);
-    for (uint64_t* b : {&sy->p_ready, &sy->q_free}) mbar_init(smem_u32(b), kUmmaOutWarps);
+    for (uint64_t* b : {&sy->p_ready, &sy->q_free[0], &sy->q_free[1]}) mbar_init(smem_u32(b), kUmmaOutWarps);
     sy->abort = 0;
     fence_mbar_init();
   }
