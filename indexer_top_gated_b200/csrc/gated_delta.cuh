@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
   };
   gates(a.head0 + hl0);
   __syncthreads();  // the barrier is there to wait for
-  mbar_wait_bounded(bar, 0, a.status, &sm.abort);
+  if (!mbar_wait_bounded(bar, 0, a.status, &sm.abort))
+    mbar_wait_bounded(bar, 0, nullptr, nullptr);  // not to leave with copies in flight
   if (valid < kDeltaChunk) {
     for (int i = 0; i < 4; ++i)
       delta_zero_rows(sm.k + i * (kDeltaTile / 2), 128, valid, tid, kPrepThreads);
@@ -729,15 +730,30 @@ struct ScanPlace {
   int64_t item_step;
 };
 
+// What a loader ends with: the copies of the last two of the `loaded` chunks are complete (or given
+// up), so that shared memory is not freed under them after a wait that ran out elsewhere.
+template <typename Sync>
+DSA_DEV void scan_drain(const ScanPlace& at, Sync* sy, int loaded) {
+  for (int c = loaded > 2 ? loaded - 2 : 0; c < loaded; ++c) {
+    const bool part = at.len - c * kDeltaChunk < kDeltaChunk;
+    mbar_wait_bounded(smem_u32(part ? &sy->tail : &sy->full[c & 1]), part ? 0 : c >> 1 & 1, nullptr,
+                      nullptr);
+  }
+}
+
 // The loader, one warp: chunk by chunk into the two stages as they come free.
 DSA_DEV void scan_loader(const DeltaArgs& a, const DeltaMaps& maps, const ScanPlace& at,
                          unsigned char* smem, ScanSync* sy) {
   const int lane = threadIdx.x & 31;
   const int n_chunks = (at.len + kDeltaChunk - 1) / kDeltaChunk;
-  for (int c = 0; c < n_chunks; ++c) {
+  int c = 0;
+  for (; c < n_chunks; ++c) {
     const int valid = at.len - c * kDeltaChunk;
-    if (c >= 2)
-      mbar_wait_bounded(smem_u32(&sy->empty[c & 1]), ((c >> 1) + 1) & 1, a.status, &sy->abort);
+    if (c >= 2) {
+      const bool ok =
+          mbar_wait_bounded(smem_u32(&sy->empty[c & 1]), ((c >> 1) + 1) & 1, a.status, &sy->abort);
+      if (__any_sync(~0u, !ok)) break;
+    }
     const bool part = valid < kDeltaChunk;
     const uint32_t full = smem_u32(&sy->full[c & 1]);
     const uint32_t bar = part ? smem_u32(&sy->tail) : full;
@@ -760,6 +776,7 @@ DSA_DEV void scan_loader(const DeltaArgs& a, const DeltaMaps& maps, const ScanPl
       if (lane == 0) mbar_arrive(full);
     }
   }
+  scan_drain(at, sy, c);
 }
 
 // The chain: warp w of the pair whose exchange area is ex.

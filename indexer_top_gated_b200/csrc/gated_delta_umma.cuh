@@ -242,10 +242,13 @@ DSA_DEV void umma_wait(const DeltaArgs& a, UmmaSync* sy, uint64_t& bar, uint32_t
 DSA_DEV void umma_load(const DeltaArgs& a, const DeltaMaps& maps, const ScanPlace& at,
                        unsigned char* smem, UmmaSync* sy) {
   const int lane = threadIdx.x & 31;
+  int c = 0;
 #pragma unroll 1
-  for (int c = 0; c * kDeltaChunk < at.len; ++c) {
-    if (c >= 2)  // chunk c - 2's products are complete and its scalars and V read
+  for (; c * kDeltaChunk < at.len; ++c) {
+    if (c >= 2) {  // chunk c - 2's products are complete and its scalars and V read
       umma_wait_smem(a, sy, sy->q_free[c & 1], (c >> 1 & 1) ^ 1);
+      if (__any_sync(~0u, sy->abort)) break;
+    }
     const int valid = at.len - c * kDeltaChunk;
     const bool part = valid < kDeltaChunk;
     const uint32_t full = smem_u32(&sy->full[c & 1]);
@@ -279,10 +282,9 @@ DSA_DEV void umma_load(const DeltaArgs& a, const DeltaMaps& maps, const ScanPlac
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the UMMAs read them
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
-    } else if (sy->abort) {  // a wait ran out: let the copies end before shared memory is freed
-      mbar_wait_bounded(full, c >> 1 & 1, nullptr, nullptr);
     }
   }
+  scan_drain(at, sy, c);
 }
 
 // The issuing thread.
