@@ -731,9 +731,10 @@ struct ScanPlace {
 };
 
 // What a loader ends with: the copies of the last two of the `loaded` chunks are complete (or given
-// up), so that shared memory is not freed under them after a wait that ran out elsewhere.
+// up), so that shared memory is not freed under them after a wait that ran out elsewhere.  (Out of
+// line: in line it moved the scan's code: 4096 tokens x 8 heads 129.2 us, so 126.4.)
 template <typename Sync>
-DSA_DEV void scan_drain(const ScanPlace& at, Sync* sy, int loaded) {
+__device__ __noinline__ void scan_drain(const ScanPlace& at, Sync* sy, int loaded) {
   for (int c = loaded > 2 ? loaded - 2 : 0; c < loaded; ++c) {
     const bool part = at.len - c * kDeltaChunk < kDeltaChunk;
     mbar_wait_bounded(smem_u32(part ? &sy->tail : &sy->full[c & 1]), part ? 0 : c >> 1 & 1, nullptr,
