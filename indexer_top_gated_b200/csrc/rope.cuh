@@ -5,7 +5,7 @@
 // Bound: HBM.  Each input is read once and each output written once, 16 bytes at a time; the
 // angles of a row are formed once, in fp64 (p f_i passes 2^24 long before positions end), and
 // shared by all its heads through shared memory, so the arithmetic stays far below the copies.
-// Measured: 32768 rows of 32 query and 4 key heads and 4 indexer heads 128 us, 5.8 TB/s; 64 rows
+// Measured: 32768 rows of 32 query and 4 key heads and 4 indexer heads 127 us, 5.8 TB/s; 64 rows
 // 4.4 us.
 #pragma once
 
@@ -263,24 +263,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const __gr
                     false, 1.f);
     }
   }
+  // the indexer's heads, 4 + 4 at most: one item a thread, or none
+  static_assert(kIdxHeads >= 8, "");
+  const int vh = t / 4;
+  if (vh >= idx_heads) return;
   rope_pairs(c, ics[my], iit);
-  for (int vh = t / 4; vh < idx_heads; vh += kIdxHeads) {
-    uint4 u, w;
-    if (vh == t / 4) {
-      cp_async_wait<0>();
-      u = mine[kRopeAhead * 2 * kRopeThreads], w = mine[(kRopeAhead * 2 + 1) * kRopeThreads];
-    } else {
-      const __nv_bfloat16* src = idx_source(vh);
-      u = *reinterpret_cast<const uint4*>(src + iit.u0 * 8);
-      w = *reinterpret_cast<const uint4*>(src + iit.u1 * 8);
-    }
-    const bool first = vh < ni;
-    const RopeTensor& x = a.t[first ? 3 : 4];
-    const int64_t to = first ? q_row : c_row;
-    if (to >= 0)
-      rope_finish(x, (to * x.heads + (first ? vh : vh - ni)) * 64, iit, u, w,
-                  iit.pair0 >= 0, c, inter, a.idx_fp8, first ? a.idx_scale_q : a.idx_scale_k);
-  }
+  cp_async_wait<0>();
+  const bool first = vh < ni;
+  const RopeTensor& x = a.t[first ? 3 : 4];
+  const int64_t to = first ? q_row : c_row;
+  if (to >= 0)
+    rope_finish(x, (to * x.heads + (first ? vh : vh - ni)) * 64, iit,
+                mine[kRopeAhead * 2 * kRopeThreads], mine[(kRopeAhead * 2 + 1) * kRopeThreads],
+                iit.pair0 >= 0, c, inter, a.idx_fp8, first ? a.idx_scale_q : a.idx_scale_k);
 }
 
 }  // namespace dsa
