@@ -400,7 +400,7 @@ dsa_status dsa_decode_noalloc(const dsa_params* params, const dsa_ragged* ragged
  * linear branch, `other` of dsa_sparse_attn_gated_mix.  The pages name both and define neither;
  * the formulas below are the ones this library implements.
  * The conventions at the top hold.  Rows of a padded batch (q_offsets[batch] .. total_q-1) enter
- * no result and are not written.
+ * no result and are not written.  "Overlaps" below is judged by spans, first element to last.
  */
 
 /* Pairs of a rotated part of r dimensions: (i, i + r/2), or (2i, 2i + 1). */
@@ -539,8 +539,10 @@ typedef struct {
  *               before it, for a sequence without tokens).  May be state_in.
  *   state_index int32 [batch] or NULL, as for dsa_short_conv.
  * dsa_gated_delta_prefill takes any Q_b: sequences of up to 24 tokens run token by token, longer
- * ones in chunks of 64 (the state stays fp32; operands of the tensor-core products enter in
- * bf16 pieces that keep the state within about 1e-6 of itself).  A sequence's results do not depend
+ * ones in chunks of 64 (the state stays fp32; operands of the tensor-core products enter in bf16
+ * pieces that keep the state within about 1e-6 of itself; for the output the weights of a chunk's
+ * tokens, scale * e^(decay from j to t) * q_t.k_j, are rounded to bf16, which moves it by up to 2^-8
+ * of the sum of its terms' magnitudes).  A sequence's results do not depend
  * on the workspace's size, and on the rest of the batch only in the last bits, through the choice
  * of the kernel: one for batches whose heads fill the GPU (total_q * n_v_heads against max_q_len),
  * one for fewer.  A NaN or an infinity in a token's inputs stays in its sequence and value heads,

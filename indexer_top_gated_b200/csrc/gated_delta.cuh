@@ -9,7 +9,7 @@
 // Recurrent form (delta_recurrent_kernel): decode and sequences of few tokens.  What it cannot
 // do without is the state, 64 KB a head in and out; a warp keeps 16 rows of it in registers, so
 // the state crosses HBM once each way however many tokens the sequence has.  Measured: 256
-// sequences x 64 heads 326 us, 6.6 TB/s; 64 x 32 heads 44 us, 6.1 TB/s.
+// sequences x 64 heads 326 us, 6.6 TB/s; 64 x 32 heads 46 us, 5.8 TB/s.
 //
 // Chunked form: with G the running sum of g inside a chunk of 64 tokens,
 //   (I + A) U = diag(beta) (V - diag(e^G) K S0^T),  A_ij = beta_i e^(G_i - G_j) k_i.k_j (j < i)
@@ -26,8 +26,11 @@
 // tensor cores take bf16, so an fp32 operand enters as two or three bf16 pieces (8 mantissa bits
 // each): k, q and v are bf16 already and enter whole.  S in K S0^T has two pieces (the third
 // moves the state by 1e-7 of itself), T, V - K S0^T and U have three, which leaves the state
-// 1e-7 to 1e-6 off, as fp32 products would; with two it is 5e-6 off.  The output is rounded to
-// bf16: P enters rounded once and U with two pieces, an error no larger than that rounding's.
+// 1e-7 to 1e-6 off, as fp32 products would; with two it is 5e-6 off.  Decays inside a chunk are
+// powers of two by ex2.approx (2^-22 off).  The output is rounded to bf16 once, and U and S enter its
+// products with two pieces (2^-16); but P is kept as one bf16, which moves an output by up to 2^-8 of
+// sum_j |P_ij U_j|: with the output's own rounding 2.3e-3 in all (2-norm), 1.7e-3 without.  A second
+// piece of P would be another 5 KB of an item's 21 (written and read once each) and a third product.
 #pragma once
 
 #include <cstddef>
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prep_kernel(
 // next limit (304 a scheduler and chunk).  So accumulators alternate, eight or six between two
 // uses of one, and operands are fetched one step ahead.  Measured: a chunk takes 1.65 us with one
 // set of warps a CTA (8 heads), 2.1 us with two (32 heads: tensor pipe 63 %, shared-memory pipe
-// 72 %); 32768 tokens x 32 heads 1.40 ms with the preparation.
+// 72 %); 32768 tokens x 32 heads 1.36 ms with the preparation.
 constexpr int kScanNV = 32;  // value columns of a V tile
 // one chunk's operands: K, Q, V, the workspace item
 constexpr int kScanV = 2 * kDeltaTile;
