@@ -236,9 +236,9 @@ constexpr int kConvRun = 48;  // rows of a run in a large batch
 template <int W>
 dsa_status launch_conv(const ConvArgs& a, const dsa_ragged* R, int sms, cudaStream_t st) {
   const int groups = (a.channels / 8 + kConvThreads - 1) / kConvThreads;
-  // Long runs read fewer rows twice; short ones spread a small batch over the GPU (8192 channels,
-  // runs of 8 and of 48 rows: 300 rows 6.7 and 13.0 us, 1500 rows 16.4 and 14.9 us, 8000 rows 91
-  // and 65 us)
+  // Long runs read fewer rows twice; short ones spread a small batch over the GPU (4 taps, 8192
+  // channels, runs of 8 and of 48 rows: 300 rows 6.2 and 9.6 us, 900 rows 11.6 and 11.2 us, 1500
+  // rows 16.7 and 14.0 us, 8000 rows 66 and 49 us; 2 taps, one row twice: 8000 rows 44 and 48 us)
   const bool wide = R->total_q / kConvRun * groups * 2 >= 3 * (int64_t)sms;
   // (max_q_len may be unset: either form takes sequences of any length)
   const bool single = R->max_q_len == 1;

@@ -2,8 +2,8 @@
 // is filtered over its own last W rows,
 //   y[t,c] = act(bias[c] + sum_{j < W} w[c,j] x[t - W + 1 + j, c]),
 // the rows before a sequence's first coming from its state (W - 1 rows, newest last).
-// Bound: HBM, closely followed by instruction issue (an exponential and a reciprocal for each
-// activation).  A thread walks a run of rows of 8 channels (48, in small batches 8, 1 for single
+// Bound: HBM, closely followed by the special-function pipe (74 %: an exponential and a reciprocal
+// for each activation).  A thread walks a run of rows of 8 channels (48, in small batches 8, 1 for single
 // tokens) with the window in registers, so a row is read once (and W - 1 rows again where a run
 // begins).  Measured: 32768 rows x 8192 channels 172 us, 6.2 TB/s.
 #pragma once
