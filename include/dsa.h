@@ -554,7 +554,9 @@ typedef struct {
  *               passes as that needs, the recommended size holds all).  0 bytes, and NULL, when
  *               max_q_len <= 24.  Calls that can overlap on the GPU (other streams, captured
  *               graphs that replay at once) need a workspace each.
- * Only batch, q_offsets, max_q_len, total_q and q_offsets_host of dsa_ragged are read.
+ * Only batch, q_offsets, max_q_len, total_q and q_offsets_host of dsa_ragged are read.  A captured
+ * call keeps what it planned from q_offsets_host (whether there are sequences of up to 24 tokens):
+ * where lengths change between replays, leave it NULL.
  * Requirements: pointers 16-byte aligned, row strides multiples of 8; out overlaps no input and
  * no state; state_out is state_in or does not overlap it.
  */
